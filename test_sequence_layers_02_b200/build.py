@@ -18,7 +18,10 @@ UNITS = [(CSRC / "ttt_scan.cu", "ttt_scan", ()),
          (CSRC / "backward.cu", "backward", ()),
          (CSRC / "probe.cu", "probe", ()),
          (CSRC / "tc_many.cu", "tc_many", ()),
-         (CSRC / "host_scan.cu", "host_scan", ())]
+         (CSRC / "host_scan.cu", "host_scan", ()),
+         (CSRC / "conv.cu", "conv", ()),
+         (CSRC / "ssm.cu", "ssm", ()),
+         (CSRC / "norm.cu", "norm", ())]
 UNITS += [(CSRC / "simt.cu", f"simt_{dt}_{md}",
            (f"-DTTT_SIMT_BF16={int(dt == 'bf16')}", f"-DTTT_SIMT_MINIBATCH={int(md == 'mb')}"))
           for dt in ("f32", "bf16") for md in ("tok", "mb")]

@@ -1,0 +1,97 @@
+// Device helpers shared by the operators around the scan (convolution, selective
+// scan, norm), and the launch of their fixed-order reductions.
+#pragma once
+
+#include "common.cuh"
+
+namespace ttt {
+
+// 2^x on the special-function unit: relative error at most 2^-22, denormal results are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + exp(-x)) from one ex2 and one reciprocal, a few units in the last place
+// off; exp(-x) = inf gives 0.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __fdividef(1.0f, 1.0f + ex2(-kLog2e * x));
+}
+
+// log(1 + exp(x)), accurate in the relative sense on both sides (a step size of
+// 1e-3 needs log1p: 1 + e would keep 4 of its digits).
+__device__ __forceinline__ float softplus(float x) {
+  return fmaxf(x, 0.0f) + log1pf(ex2(-kLog2e * fabsf(x)));
+}
+
+// Load VEC consecutive elements, widened to fp32. VEC > 1 needs the address
+// aligned to VEC elements (16 bytes at most per access).
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&out)[VEC]) {
+  if constexpr (VEC == 1) {
+    out[0] = to_f32(p[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      out[i] = x.x; out[i + 1] = x.y; out[i + 2] = x.z; out[i + 3] = x.w;
+    }
+  } else {
+    static_assert(VEC == 4 || VEC == 8, "bf16 vectors of 4 or 8");
+    uint32_t w[VEC / 2];
+    if constexpr (VEC == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x; w[1] = x.y;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      out[2 * i] = __uint_as_float(w[i] << 16);
+      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
+  if constexpr (VEC == 1) {
+    p[0] = from_f32<T>(x[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else if constexpr (VEC == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                              pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  } else {
+    static_assert(VEC == 4, "bf16 vectors of 4 or 8");
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  }
+}
+
+// Sum of `parts` rows of n floats, in row order within each of 32 interleaved
+// strands and then over the strands: the same bits on every call. Column i goes
+// to the segment that holds it (up to three outputs laid end to end); a null
+// output is skipped.
+struct ReduceOut {
+  float* p[3];
+  long long n[3];
+};
+
+__global__ void reduce_parts_kernel(const float* part, int parts, long long n, ReduceOut out);
+
+// Enqueue it (defined in conv.cu).
+int launch_reduce_parts(const float* part, int parts, long long n, const ReduceOut& out,
+                        cudaStream_t stream);
+
+}  // namespace ttt

@@ -1,0 +1,325 @@
+// C-ABI entry points of the selective state space scan (include/ttt_ssm.h):
+// argument checks, how far a prompt's tokens are split over CTAs, launches.
+#include "ttt_ssm.h"
+#include "abi_util.h"
+#include "launch.h"
+#include "ssm_bwd.cuh"
+
+static_assert(ttt::kSsmTile == TTT_SSM_CHUNK, "a snapshot for every tile");
+
+namespace {
+
+using ttt::SsmParams;
+using ttt::abi::misaligned;
+using ttt::abi::misaligned_to;
+using ttt::abi::Span;
+using ttt::abi::Strided;
+
+constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_SSM_SOFTPLUS;
+constexpr int kMaxGridY = 65535;
+
+int check_sizes(int B, int T, int D, int G, int N, unsigned mode) {
+  if (mode & ~kKnownModes) return TTT_ERR_INVALID_ARG;
+  if (B < 0 || T < 0 || D < 1 || G < 1 || N < 1 || D % G != 0) return TTT_ERR_INVALID_ARG;
+  if (N != 8 && N != 16 && N != 32 && N != 64) return TTT_ERR_UNSUPPORTED;
+  if ((long long)D * N > 0x7fffffffLL || (long long)G * N > 0x7fffffffLL)
+    return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+int threads_per_channel(int N) { return N / 4; }
+
+int channel_tiles(int D, int G, int N, int threads) {
+  const int ch = threads / threads_per_channel(N);
+  return (D / G + ch - 1) / ch;
+}
+
+int split_for(long long ctas, int T, int sms) {
+  const int tiles = (T + ttt::kSsmTile - 1) / ttt::kSsmTile;
+  int s = 1;
+  while (s < ttt::kSsmMaxSplit && ctas * s * 2 <= 4LL * sms && tiles >= 8 * s) s *= 2;
+  return s;
+}
+
+int sm_count() {
+  const int n = ttt::device_sm_count();
+  return n > 0 ? n : 148;
+}
+
+template <typename Kernel>
+int launch_kernel(Kernel kernel, long long blocks, int split, int B, int threads, size_t smem,
+                  const SsmParams& p, cudaStream_t s) {
+  if (blocks * split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+    return TTT_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(blocks * split), B < kMaxGridY ? B : kMaxGridY);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+template <int L, typename InT>
+int launch_fwd(const SsmParams& p, cudaStream_t s) {
+  using S = ttt::SsmFwdShape<L>;
+  const long long blocks = (long long)p.tiles * p.G;
+  return p.split > 1
+             ? launch_kernel(ttt::ssm_fwd_kernel<L, InT, true>, blocks, p.split, p.B, S::NT, 0, p, s)
+             : launch_kernel(ttt::ssm_fwd_kernel<L, InT, false>, blocks, 1, p.B, S::NT, 0, p, s);
+}
+
+template <int L, typename InT>
+int launch_bwd(const SsmParams& p, cudaStream_t s) {
+  using S = ttt::SsmBwdShape<L>;
+  const long long blocks = (long long)p.tiles * p.G;
+  constexpr size_t smem = sizeof(typename S::Smem);
+  return p.split > 1
+             ? launch_kernel(ttt::ssm_bwd_kernel<L, InT, true>, blocks, p.split, p.B, S::NT, smem, p, s)
+             : launch_kernel(ttt::ssm_bwd_kernel<L, InT, false>, blocks, 1, p.B, S::NT, smem, p, s);
+}
+
+template <int L, typename InT>
+int launch_step(const SsmParams& p, cudaStream_t s) {
+  const long long blocks = ((long long)p.D * L + 255) / 256;
+  ttt::ssm_step_kernel<L, InT>
+      <<<dim3((unsigned)blocks, p.B < kMaxGridY ? p.B : kMaxGridY), 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+enum Which { kForward, kBackward, kStep };
+
+template <Which W, int L, typename InT>
+int launch_one(const SsmParams& p, cudaStream_t s) {
+  if constexpr (W == kForward) return launch_fwd<L, InT>(p, s);
+  if constexpr (W == kBackward) return launch_bwd<L, InT>(p, s);
+  return launch_step<L, InT>(p, s);
+}
+
+template <Which W, typename InT>
+int dispatch_n(const SsmParams& p, int N, cudaStream_t s) {
+  switch (N) {
+    case 8: return launch_one<W, 2, InT>(p, s);
+    case 16: return launch_one<W, 4, InT>(p, s);
+    case 32: return launch_one<W, 8, InT>(p, s);
+    default: return launch_one<W, 16, InT>(p, s);
+  }
+}
+
+template <Which W>
+int dispatch(const SsmParams& p, int N, unsigned mode, cudaStream_t s) {
+  return (mode & TTT_IN_BF16) ? dispatch_n<W, __nv_bfloat16>(p, N, s) : dispatch_n<W, float>(p, N, s);
+}
+
+// Strides of a prompt's tensors into p (null: contiguous).
+void set_strides(SsmParams& p, int T, int D, int G, int N, const long long* s) {
+  const long long tok = (long long)T * D, vec = (long long)T * G * N;
+  if (s) {
+    p.u_b = s[0]; p.u_t = s[1]; p.d_b = s[2]; p.d_t = s[3]; p.z_b = s[4]; p.z_t = s[5];
+    p.Bm_b = s[6]; p.Bm_t = s[7]; p.Bm_g = s[8]; p.Cm_b = s[9]; p.Cm_t = s[10]; p.Cm_g = s[11];
+    p.y_b = s[12]; p.y_t = s[13];
+  } else {
+    p.u_b = p.d_b = p.z_b = p.y_b = tok;
+    p.u_t = p.d_t = p.z_t = p.y_t = D;
+    p.Bm_b = p.Cm_b = vec;
+    p.Bm_t = p.Cm_t = (long long)G * N;
+    p.Bm_g = p.Cm_g = N;
+  }
+}
+
+struct Tensors {
+  Strided u, delta, z, Bm, Cm, y;
+  bool negative() const {
+    return u.negative() || delta.negative() || z.negative() || Bm.negative() || Cm.negative() ||
+           y.negative();
+  }
+};
+
+Tensors tensors(const SsmParams& p, int B, int T, int D, int G, int N, size_t ie, size_t oe) {
+  return {{{B, T, 1}, {p.u_b, p.u_t, 0}, D, ie},          {{B, T, 1}, {p.d_b, p.d_t, 0}, D, ie},
+          {{B, T, 1}, {p.z_b, p.z_t, 0}, D, ie},          {{B, T, G}, {p.Bm_b, p.Bm_t, p.Bm_g}, N, ie},
+          {{B, T, G}, {p.Cm_b, p.Cm_t, p.Cm_g}, N, ie},   {{B, T, 1}, {p.y_b, p.y_t, 0}, D, oe}};
+}
+
+size_t par_floats(int B, int D, int N) { return (size_t)B * ttt::kSsmMaxSplit * D * (N + 2); }
+size_t bc_floats(int B, int T, int D, int G, int N) {
+  return (size_t)channel_tiles(D, G, N, 256) * B * T * G * 2 * N;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ttt_ssm_forward(const void* u, const void* delta, const float* A, const void* Bm,
+                    const void* Cm, const float* skip, const void* z, const float* delta_bias,
+                    const float* h0, const int* lengths, int B, int T, int D, int G, int N,
+                    unsigned mode, const long long* strides, void* y, float* h_T,
+                    float* h_chunks, void* cuda_stream) {
+  if (const int rc = check_sizes(B, T, D, G, N, mode)) return rc;
+  const size_t ie = (mode & TTT_IN_BF16) ? 2 : 4, oe = (mode & TTT_OUT_BF16) ? 2 : 4;
+  if (B > 0 && (!A || !h_T || (T > 0 && (!u || !delta || !Bm || !Cm || !y))))
+    return TTT_ERR_INVALID_ARG;
+  if (misaligned(A) || misaligned(h0) || misaligned(h_T) || misaligned(h_chunks) ||
+      misaligned_to(skip, 4) || misaligned_to(delta_bias, 4) || misaligned_to(lengths, 4) ||
+      misaligned_to(u, ie) || misaligned_to(delta, ie) || misaligned_to(z, ie) ||
+      misaligned_to(Bm, ie) || misaligned_to(Cm, ie) || misaligned_to(y, oe))
+    return TTT_ERR_INVALID_ARG;
+  SsmParams p{};
+  set_strides(p, T, D, G, N, strides);
+  const Tensors ts = tensors(p, B, T, D, G, N, ie, oe);
+  if (ts.negative() || ts.y.self_overlap()) return TTT_ERR_INVALID_ARG;
+  const size_t state = (size_t)B * D * N * 4;
+  const size_t n_chunks = ((size_t)T + ttt::kSsmTile - 1) / ttt::kSsmTile;
+  const Span in[] = {{u, ts.u.extent()}, {delta, ts.delta.extent()}, {z, ts.z.extent()},
+                     {Bm, ts.Bm.extent()}, {Cm, ts.Cm.extent()}, {A, (size_t)D * N * 4},
+                     {skip, (size_t)D * 4}, {delta_bias, (size_t)D * 4},
+                     {h0 == h_T ? nullptr : h0, state}, {lengths, (size_t)B * 4}};
+  const Span out[] = {{y, ts.y.extent()}, {h_T, state}, {h_chunks, state * n_chunks}};
+  if (ttt::abi::any_overlap(in, out)) return TTT_ERR_INVALID_ARG;
+  if (B == 0) return TTT_OK;
+
+  p.u = u; p.delta = delta; p.z = z; p.Bm = Bm; p.Cm = Cm;
+  p.A = A; p.skip = skip; p.delta_bias = delta_bias; p.h0 = h0; p.lengths = lengths;
+  p.y = y; p.h_T = h_T; p.h_chunks = h_chunks;
+  p.B = B; p.T = T; p.D = D; p.G = G;
+  p.per_group = D / G;
+  p.tiles = channel_tiles(D, G, N, 128);
+  p.split = split_for((long long)p.tiles * G * B, T, sm_count());
+  p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
+  p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  return dispatch<kForward>(p, N, mode, static_cast<cudaStream_t>(cuda_stream));
+}
+
+size_t ttt_ssm_backward_workspace_bytes(int B, int T, int D, int G, int N) {
+  if (B <= 0 || T < 0 || D < 1 || G < 1 || D % G != 0) return 0;
+  if (N != 8 && N != 16 && N != 32 && N != 64) return 0;
+  return (bc_floats(B, T, D, G, N) + par_floats(B, D, N)) * sizeof(float);
+}
+
+int ttt_ssm_backward(const void* u, const void* delta, const float* A, const void* Bm,
+                     const void* Cm, const float* skip, const void* z, const float* delta_bias,
+                     const int* lengths, int B, int T, int D, int G, int N, unsigned mode,
+                     const long long* strides, const float* h_chunks, const void* dy,
+                     const float* dh_T, void* du, void* ddelta, float* dA, void* dBm, void* dCm,
+                     float* dskip, void* dz, float* d_delta_bias, float* dh0, void* workspace,
+                     size_t workspace_bytes, void* cuda_stream) {
+  if (const int rc = check_sizes(B, T, D, G, N, mode)) return rc;
+  const size_t ie = (mode & TTT_IN_BF16) ? 2 : 4, oe = (mode & TTT_OUT_BF16) ? 2 : 4;
+  const bool toks = B > 0 && T > 0;
+  if (!dA || (B > 0 && (!A || !workspace))) return TTT_ERR_INVALID_ARG;
+  if (toks && (!u || !delta || !Bm || !Cm || !h_chunks || !dy || !du || !ddelta || !dBm || !dCm))
+    return TTT_ERR_INVALID_ARG;
+  if (toks && ((z != nullptr) != (dz != nullptr))) return TTT_ERR_INVALID_ARG;
+  if (misaligned(A) || misaligned(h_chunks) || misaligned(dh_T) || misaligned(dh0) ||
+      misaligned(workspace) || misaligned_to(dA, 4) || misaligned_to(skip, 4) ||
+      misaligned_to(delta_bias, 4) || misaligned_to(lengths, 4) || misaligned_to(dskip, 4) ||
+      misaligned_to(d_delta_bias, 4) || misaligned_to(u, ie) || misaligned_to(delta, ie) ||
+      misaligned_to(z, ie) || misaligned_to(Bm, ie) || misaligned_to(Cm, ie) ||
+      misaligned_to(dy, oe) || misaligned_to(du, ie) || misaligned_to(ddelta, ie) ||
+      misaligned_to(dz, ie) || misaligned_to(dBm, ie) || misaligned_to(dCm, ie))
+    return TTT_ERR_INVALID_ARG;
+  const size_t need = ttt_ssm_backward_workspace_bytes(B, T, D, G, N);
+  if (workspace_bytes < need) return TTT_ERR_INVALID_ARG;
+  SsmParams p{};
+  set_strides(p, T, D, G, N, strides);
+  const Tensors ts = tensors(p, B, T, D, G, N, ie, oe);
+  if (ts.negative()) return TTT_ERR_INVALID_ARG;
+  const size_t state = (size_t)B * D * N * 4, par = (size_t)D * N * 4;
+  const size_t n_chunks = ((size_t)T + ttt::kSsmTile - 1) / ttt::kSsmTile;
+  const size_t tok = (size_t)B * T * D * ie, vec = (size_t)B * T * G * N * ie;
+  const Span in[] = {{u, ts.u.extent()}, {delta, ts.delta.extent()}, {z, ts.z.extent()},
+                     {Bm, ts.Bm.extent()}, {Cm, ts.Cm.extent()}, {A, par},
+                     {skip, (size_t)D * 4}, {delta_bias, (size_t)D * 4},
+                     {lengths, (size_t)B * 4}, {h_chunks, state * n_chunks},
+                     {dy, ts.y.extent()}, {dh_T, state}};
+  const Span out[] = {{du, tok}, {ddelta, tok}, {dz, tok}, {dBm, vec}, {dCm, vec}, {dA, par},
+                      {dskip, (size_t)D * 4}, {d_delta_bias, (size_t)D * 4}, {dh0, state},
+                      {workspace, need}};
+  if (ttt::abi::any_overlap(in, out)) return TTT_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (B == 0) {
+    if (cudaMemsetAsync(dA, 0, par, s) != cudaSuccess ||
+        (dskip && cudaMemsetAsync(dskip, 0, (size_t)D * 4, s) != cudaSuccess) ||
+        (d_delta_bias && cudaMemsetAsync(d_delta_bias, 0, (size_t)D * 4, s) != cudaSuccess))
+      return TTT_ERR_CUDA;
+    return TTT_OK;
+  }
+
+  p.u = u; p.delta = delta; p.z = z; p.Bm = Bm; p.Cm = Cm;
+  p.A = A; p.skip = skip; p.delta_bias = delta_bias; p.lengths = lengths;
+  p.h_chunks = const_cast<float*>(h_chunks);
+  p.dy = dy; p.dh_T = dh_T; p.du = du; p.ddelta = ddelta; p.dz = dz; p.dh0 = dh0;
+  p.part_bc = static_cast<float*>(workspace);
+  p.part_par = p.part_bc + bc_floats(B, T, D, G, N);
+  p.B = B; p.T = T; p.D = D; p.G = G;
+  p.per_group = D / G;
+  p.tiles = channel_tiles(D, G, N, 256);
+  p.split = split_for((long long)p.tiles * G * B, T, sm_count());
+  p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
+  p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  const size_t bc = (size_t)B * T * G * 2 * N;
+  const size_t bc_blocks = (bc / 4 + 255) / 256;
+  if (bc_blocks > 0x7fffffffULL || (long long)B * p.split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+  int rc = dispatch<kBackward>(p, N, mode, s);
+  if (rc != TTT_OK) return rc;
+  if (bc_blocks > 0) {
+    if (mode & TTT_IN_BF16)
+      ttt::ssm_sum_bc_kernel<<<(unsigned)bc_blocks, 256, 0, s>>>(
+          p.part_bc, p.tiles, B, T, G, N, lengths, static_cast<__nv_bfloat16*>(dBm),
+          static_cast<__nv_bfloat16*>(dCm));
+    else
+      ttt::ssm_sum_bc_kernel<<<(unsigned)bc_blocks, 256, 0, s>>>(
+          p.part_bc, p.tiles, B, T, G, N, lengths, static_cast<float*>(dBm),
+          static_cast<float*>(dCm));
+    if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+  }
+  const long long dn = (long long)D * N;
+  return ttt::launch_reduce_parts(p.part_par, B * p.split, dn + 2LL * D,
+                                  {{dA, dskip, d_delta_bias}, {dn, D, D}}, s);
+}
+
+int ttt_ssm_step(const void* u, const void* delta, const float* A, const void* Bm,
+                 const void* Cm, const float* skip, const void* z, const float* delta_bias,
+                 float* h, const unsigned char* active, int B, int D, int G, int N,
+                 unsigned mode, const long long* strides, void* y, void* cuda_stream) {
+  if (const int rc = check_sizes(B, 1, D, G, N, mode)) return rc;
+  const size_t ie = (mode & TTT_IN_BF16) ? 2 : 4, oe = (mode & TTT_OUT_BF16) ? 2 : 4;
+  if (B > 0 && (!u || !delta || !A || !Bm || !Cm || !h || !y)) return TTT_ERR_INVALID_ARG;
+  if (misaligned(A) || misaligned(h) || misaligned_to(skip, 4) || misaligned_to(delta_bias, 4) ||
+      misaligned_to(u, ie) || misaligned_to(delta, ie) || misaligned_to(z, ie) ||
+      misaligned_to(Bm, ie) || misaligned_to(Cm, ie) || misaligned_to(y, oe))
+    return TTT_ERR_INVALID_ARG;
+  SsmParams p{};
+  if (strides) {
+    const long long full[14] = {strides[0], 0, strides[1], 0, strides[2], 0, strides[3], 0,
+                                strides[4], strides[5], 0, strides[6], strides[7], 0};
+    set_strides(p, 1, D, G, N, full);
+  } else {
+    set_strides(p, 1, D, G, N, nullptr);
+  }
+  const Tensors ts = tensors(p, B, 1, D, G, N, ie, oe);
+  if (ts.negative() || ts.y.self_overlap()) return TTT_ERR_INVALID_ARG;
+  const Span in[] = {{u, ts.u.extent()}, {delta, ts.delta.extent()}, {z, ts.z.extent()},
+                     {Bm, ts.Bm.extent()}, {Cm, ts.Cm.extent()}, {A, (size_t)D * N * 4},
+                     {skip, (size_t)D * 4}, {delta_bias, (size_t)D * 4}, {active, (size_t)B}};
+  const Span out[] = {{y, ts.y.extent()}, {h, (size_t)B * D * N * 4}};
+  if (ttt::abi::any_overlap(in, out)) return TTT_ERR_INVALID_ARG;
+  if (B == 0) return TTT_OK;
+
+  p.u = u; p.delta = delta; p.z = z; p.Bm = Bm; p.Cm = Cm;
+  p.A = A; p.skip = skip; p.delta_bias = delta_bias; p.active = active; p.h_T = h; p.y = y;
+  p.B = B; p.T = 1; p.D = D; p.G = G;
+  p.per_group = D / G;
+  p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
+  p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  return dispatch<kStep>(p, N, mode, static_cast<cudaStream_t>(cuda_stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,162 @@
+"""Root-mean-square norm between two blocks (``include/ttt_norm.h``):
+
+    s = x + residual,   y = s / sqrt(mean(s^2) + eps) * weight
+
+with y in fp32 or bf16 (``rmsnorm``, and ``rmsnorm_backward`` for training) or in 8 bits with scales for the
+projections behind it (``rmsnorm_fp8``). Rows are the last dimension; they are contiguous, and a
+2-D tensor may have any row stride. CUDA tensors only; see ``_binding`` for streams. There is no CPU
+fallback.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from ._binding import (Library, On, check, check_device, check_dtype, check_whole, out_dtype_of,
+                       raise_for)
+from .ttt_scan import IN_BF16, OUT_BF16
+
+NORM_SUM_BF16 = 1 << 18
+NORM_Y_E4M3 = 1 << 19
+
+_vp, _i, _u, _f, _z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float,
+                       ctypes.c_size_t)
+_lib = Library({
+    "ttt_norm_forward": ([_vp] * 3 + [_i, _i, _f, _u, _i] + [_vp] * 5, _i),
+    "ttt_norm_backward_workspace_bytes": ([_i, _i], _z),
+    "ttt_norm_backward": ([_vp] * 4 + [_i, _i, _f, _u] + [_vp] * 4 + [_z, _vp], _i),
+})
+
+
+def _rows(name, t, shape, dtype, dev):
+    """The row stride of a tensor of this shape, after its checks."""
+    check(name, t, shape, dtype, dev)
+    if t.dim() == 2:
+        return t.stride(0) if t.shape[0] > 1 else shape[-1]
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {tuple(shape)} (2-D tensors may have strides)")
+    return shape[-1]
+
+
+def _strides(D, *lds):
+    return None if all(v == D for v in lds) else (ctypes.c_longlong * 4)(*lds)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _forward(x, weight, residual, eps, mode, group, y, y_dtype, s, scale_shape, stream):
+    dev, dtype = check_device("x", x), check_dtype("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    shape = x.shape
+    D = shape[-1]
+    M = x.numel() // D if D else 0
+    w = check_whole("weight", weight, (D,), torch.float32, dev)
+    ld_x = _rows("x", x, shape, dtype, dev)
+    sum_dtype, ld_r = dtype, D
+    if residual is not None:
+        sum_dtype = check_dtype("residual", residual)
+        ld_r = _rows("residual", residual, shape, sum_dtype, dev)
+    elif s is not None:
+        raise ValueError("s: there is none without a residual (it would be x)")
+    mode |= ((IN_BF16 if dtype == torch.bfloat16 else 0) |
+             (NORM_SUM_BF16 if sum_dtype == torch.bfloat16 else 0))
+    scale = None
+    with On(dev, stream, (x, weight, residual, y, s)) as st:
+        if y is None:
+            y = torch.empty(shape, dtype=y_dtype, device=dev)
+        ld_y = _rows("y", y, shape, y_dtype, dev)
+        ld_s = D
+        if residual is not None:
+            if s is None:
+                s = torch.empty(shape, dtype=sum_dtype, device=dev)
+            ld_s = _rows("s", s, shape, sum_dtype, dev)
+        if scale_shape is not None:
+            scale = torch.empty(shape[:-1] + scale_shape, dtype=torch.float32, device=dev)
+        rc = _lib().ttt_norm_forward(x.data_ptr(), _ptr(residual), w, M, D, eps, mode, group,
+                                     _strides(D, ld_x, ld_r, ld_y, ld_s), y.data_ptr(), _ptr(s),
+                                     _ptr(scale), st)
+    raise_for(rc, "ttt_norm_forward")
+    return y, scale, x if residual is None else s
+
+
+def rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, out_dtype: Optional[torch.dtype] = None,
+            y: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+            stream: Optional[torch.cuda.Stream] = None):
+    """``(y, s) = rmsnorm(x, weight, residual)``.
+
+    x: [..., D] fp32 or bf16, D up to 16384; weight: [D] fp32; residual: [..., D] fp32 or bf16 (its own
+    type) or None. y: ``out_dtype``, default x's type, of the unrounded sum; s: the sum in the
+    residual's type, or x itself without a residual. ``s`` may be given as the residual (or as x, where the
+    types agree) to update the residual stream in place.
+    """
+    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, check_dtype("x", x))
+    mode = OUT_BF16 if out_dtype == torch.bfloat16 else 0
+    y, _, s = _forward(x, weight, residual, eps, mode, 0, y, out_dtype, s, None, stream)
+    return y, s
+
+
+def rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
+                y: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """``(y, scale, s) = rmsnorm_fp8(x, weight, residual)``: y as float8_e4m3fn codes.
+
+    scale: fp32 [..., 1], the row's max |y| / 448 (``group=0``), or [..., ceil(D / 128)], that of each 128
+    columns (``group=128``); the value of a code is code * scale. Otherwise as ``rmsnorm``.
+    """
+    if group not in (0, 128):
+        raise ValueError("group: expected 0 (a scale per row) or 128")
+    n = -(-x.shape[-1] // 128) if group and x.dim() else 1
+    return _forward(x, weight, residual, eps, NORM_Y_E4M3, group, y, torch.float8_e4m3fn, s, (n,),
+                    stream)
+
+
+def backward_workspace_bytes(M: int, D: int) -> int:
+    """Bytes of device workspace ``ttt_norm_backward`` needs for M rows."""
+    return int(_lib().ttt_norm_backward_workspace_bytes(M, D))
+
+
+def rmsnorm_backward(dy, s, weight, ds=None, *, eps: float = 1e-6,
+                     dx: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of ``<dy, y> + <ds, s>`` for ``(y, s) = rmsnorm(x, weight, residual)``.
+
+    dy: [..., D] fp32 or bf16; s: as ``rmsnorm`` returned it (the gradient is taken at these, rounded
+    values); ds: the gradient that reaches s from elsewhere, s's type, or None. Returns dx, the gradient
+    of x and of the residual alike (s's type; may be given as ``ds`` itself), and dweight (fp32).
+    ``workspace`` (optional): at least ``backward_workspace_bytes`` bytes, not shared by calls that
+    overlap.
+    """
+    dev, dtype = check_device("s", s), check_dtype("s", s)
+    if s.dim() < 1:
+        raise ValueError("s must be [..., D]")
+    shape = s.shape
+    D = shape[-1]
+    M = s.numel() // D if D else 0
+    w = check_whole("weight", weight, (D,), torch.float32, dev)
+    ld_s = _rows("s", s, shape, dtype, dev)
+    ld_g = _rows("dy", dy, shape, check_dtype("dy", dy), dev)
+    ld_e = D if ds is None else _rows("ds", ds, shape, dtype, dev)
+    mode = ((OUT_BF16 if dy.dtype == torch.bfloat16 else 0) |
+            (NORM_SUM_BF16 if dtype == torch.bfloat16 else 0))
+    with On(dev, stream, (dy, s, weight, ds, dx, workspace)) as st:
+        if dx is None:
+            dx = torch.empty(shape, dtype=dtype, device=dev)
+        ld_o = _rows("dx", dx, shape, dtype, dev)
+        need = backward_workspace_bytes(M, D)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        check_whole("workspace", workspace, workspace.shape, workspace.dtype, dev)
+        dweight = torch.empty_like(weight)
+        rc = _lib().ttt_norm_backward(dy.data_ptr(), s.data_ptr(), w, _ptr(ds), M, D, eps, mode,
+                                      _strides(D, ld_g, ld_s, ld_e, ld_o), dx.data_ptr(),
+                                      dweight.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), st)
+    raise_for(rc, "ttt_norm_backward")
+    return dict(dx=dx, dweight=dweight)
