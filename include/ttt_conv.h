@@ -38,7 +38,9 @@ extern "C" {
 /* Mode bits, beside TTT_IN_BF16 (x, state, dx, dstate are bf16, else fp32) and
  * TTT_OUT_BF16 (y and dy are bf16, else fp32). */
 enum {
-  TTT_CONV_SILU = 1u << 16 /* y = SiLU(pre) */
+  TTT_CONV_SILU = 1u << 16,    /* y = SiLU(pre) */
+  TTT_CONV_PAD_ZERO = 1u << 20 /* y is set to 0 behind a row's length and in rows that are not
+                                  active, else left as it was there (ignored by the backward) */
 };
 
 /*
@@ -48,8 +50,8 @@ enum {
  *   bias     [H, d]           fp32, contiguous; NULL = 0
  *   state    [B, H, K-1, d]   type of x, oldest first; NULL = zeros
  *   lengths  [B]              int32 tokens of each row, clipped to [0, T]; NULL = T.
- *                             Tokens at or past the length are not read, and y is left as
- *                             it was there.
+ *                             Tokens at or past the length are not read, and y is left as it
+ *                             was there (or 0 with TTT_CONV_PAD_ZERO).
  *   y        [B, H, T, d]     out: fp32, or bf16 with TTT_OUT_BF16
  *   state_T  [B, H, K-1, d]   out, or NULL; may be `state` itself (same strides)
  *   strides  NULL = all contiguous, or 12 element counts: between batch rows, heads and
@@ -82,8 +84,8 @@ int ttt_conv_backward(const void* x, const float* weight, const float* bias, con
 
 /*
  * One token of every row: x, y [B, H, d]; state [B, H, K-1, d] is read and moved
- * on by one IN PLACE. active [B] bytes or NULL: 0 = the row's y and state are left as
- * they were. strides: NULL or 7 element counts, between rows and heads of x and of y, and
+ * on by one IN PLACE. active [B] bytes or NULL: 0 = the row's state is left bit for bit, and its
+ * y as it was (or 0 with TTT_CONV_PAD_ZERO). strides: NULL or 7 element counts, between rows and heads of x and of y, and
  * between rows, heads and entries of state. A chain of steps equals the prompt.
  */
 int ttt_conv_step(const void* x, const float* weight, const float* bias, void* state,

@@ -30,7 +30,9 @@ extern "C" {
 /* Mode bits, beside TTT_IN_BF16 (u, delta, z, Bm, Cm and their gradients are bf16, else
  * fp32) and TTT_OUT_BF16 (y and dy are bf16, else fp32). */
 enum {
-  TTT_SSM_SOFTPLUS = 1u << 17 /* dt = softplus(delta + delta_bias) */
+  TTT_SSM_SOFTPLUS = 1u << 17, /* dt = softplus(delta + delta_bias) */
+  TTT_SSM_PAD_ZERO = 1u << 20  /* y is set to 0 behind a row's length and in rows that are not
+                                  active, else left as it was there (ignored by the backward) */
 };
 
 /* Tokens between two snapshots of the state (h_chunks). */
@@ -41,11 +43,13 @@ enum { TTT_SSM_CHUNK = 16 };
  * where noted:
  *   u, delta, z [B, T, D]   fp32, or bf16 with TTT_IN_BF16; z NULL = no output gate
  *   Bm, Cm      [B, T, G, N] same type
- *   A           [D, N]      fp32, contiguous, 16-byte aligned (finite; decays have A < 0)
+ *   A           [D, N]      fp32, contiguous, 16-byte aligned; finite, and A dt <= 0 for a state that
+ *                           decays (nothing is clipped: a growing one may leave fp32's range)
  *   skip, delta_bias [D]    fp32; NULL = 0
  *   h0          [B, D, N]   fp32, contiguous, 16-byte aligned; NULL = zeros
  *   lengths     [B]         int32 tokens of each row, clipped to [0, T]; NULL = T. Tokens at or
  *                           past the length are not read, and y is left as it was there
+ *                           (or 0 with TTT_SSM_PAD_ZERO)
  *   y           [B, T, D]   out: fp32, or bf16 with TTT_OUT_BF16
  *   h_T         [B, D, N]   out, fp32, contiguous, 16-byte aligned: the state after each row's
  *                           last token; may equal h0
@@ -53,8 +57,9 @@ enum { TTT_SSM_CHUNK = 16 };
  *               token, for the backward (slots of chunks past a row's length are left as they were)
  *   strides     NULL = all contiguous, or 14 element counts, none negative: between rows and tokens of
  *               u, of delta, of z; between rows, tokens and groups of Bm, of Cm; between rows and
- *               tokens of y. The D channels, and the N entries, are always contiguous.
- * Sizes: B, T >= 0, D >= 1, G >= 1 dividing D, N in {8, 16, 32, 64}.
+ *               tokens of y; at most 2^24 between tokens. The D channels, and the N entries, are
+ *               always contiguous.
+ * Sizes: B, T >= 0, 1 <= D <= 2^24, G >= 1 dividing D, N in {8, 16, 32, 64}.
  * The extent of an output may not meet that of an input (except h_T = h0) or of another
  * output.
  */
@@ -89,8 +94,8 @@ int ttt_ssm_backward(const void* u, const void* delta, const float* A, const voi
 
 /*
  * One token of every row: u, delta, z, y [B, D]; Bm, Cm [B, G, N]; h [B, D, N] fp32, contiguous,
- * 16-byte aligned, is read and updated IN PLACE. active [B] bytes or NULL: 0 = the row's y and h are left
- * as they were. strides: NULL or 8 element counts, between rows of u, delta, z; between rows and
+ * 16-byte aligned, is read and updated IN PLACE. active [B] bytes or NULL: 0 = the row's h is left bit for
+ * bit, and its y as it was (or 0 with TTT_SSM_PAD_ZERO). strides: NULL or 8 element counts, between rows of u, delta, z; between rows and
  * groups of Bm, of Cm; between rows of y. A chain of steps equals the prompt.
  */
 int ttt_ssm_step(const void* u, const void* delta, const float* A, const void* Bm,

@@ -18,11 +18,12 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_device, check_dtype, check_whole, out_dtype_of,
-                       raise_for, strides_of)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
+                       raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 CONV_SILU = 1 << 16
+CONV_PAD_ZERO = 1 << 20
 
 _vp, _i, _u, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
 _lib = Library({
@@ -31,28 +32,30 @@ _lib = Library({
     "ttt_conv_backward": ([_vp] * 5 + [_i] * 5 + [_u] + [_vp] * 8 + [_z, _vp], _i),
     "ttt_conv_step": ([_vp] * 5 + [_i] * 4 + [_u] + [_vp] * 3, _i),
 })
+_F32, _BF16 = torch.float32, torch.bfloat16
 _OUTER = {3: (0, 0, 1), 4: (0, 1, 2)}  # dimensions of the strides between rows, heads, tokens
 
 
-def _sizes(x, weight, bias, dev, T_dim: bool):
-    """B, H, T, d, K and the shape of the channels, (D,) or (H, d)."""
-    if x.dim() not in ((3, 4) if T_dim else (2, 3)):
-        raise ValueError("x must be [B, T, D] or [B, H, T, d]" if T_dim else
+def _sizes(x, weight, bias, dev, tokens: bool):
+    """B, H, T, d, K, the addresses of weight and bias; ``tokens``: x has a dimension of tokens."""
+    shape = x.shape
+    n = len(shape) + (0 if tokens else 1)
+    if n == 3:
+        H, channels = 1, (shape[-1],)
+    elif n == 4:
+        H, channels = shape[1], (shape[1], shape[-1])
+    else:
+        raise ValueError("x must be [B, T, D] or [B, H, T, d]" if tokens else
                          "x must be [B, D] or [B, H, d]")
-    heads = x.dim() == (4 if T_dim else 3)
-    B, d = x.shape[0], x.shape[-1]
-    H = x.shape[1] if heads else 1
-    T = x.shape[-2] if T_dim else 1
-    channels = (H, d) if heads else (d,)
     K = weight.shape[-1] if weight.dim() == len(channels) + 1 else 0
-    w = check_whole("weight", weight, channels + (K,), torch.float32, dev)
-    b = check_whole("bias", bias, channels, torch.float32, dev)
-    return B, H, T, d, K, channels, w, b
+    w = check_whole("weight", weight, channels + (K,), _F32, dev)
+    b = check_whole("bias", bias, channels, _F32, dev)
+    return shape[0], H, shape[-2] if tokens else 1, shape[-1], K, w, b
 
 
-def _mode(in_dtype, out_dtype, silu) -> int:
-    return ((IN_BF16 if in_dtype == torch.bfloat16 else 0) |
-            (OUT_BF16 if out_dtype == torch.bfloat16 else 0) | (CONV_SILU if silu else 0))
+def _mode(in_dtype, out_dtype, silu, pad_zero) -> int:
+    return ((IN_BF16 if in_dtype is _BF16 else 0) | (OUT_BF16 if out_dtype is _BF16 else 0) |
+            (CONV_SILU if silu else 0) | (CONV_PAD_ZERO if pad_zero else 0))
 
 
 def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths=None,
@@ -68,36 +71,31 @@ def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths
     values behind a row's length; one made here is 0 there. state_T, the inputs before the next
     token, may be ``state`` itself.
     """
-    dev, in_dtype = check_device("x", x), check_dtype("x", x)
-    B, H, T, d, K, channels, w, b = _sizes(x, weight, bias, dev, True)
-    check("x", x, x.shape, in_dtype, dev)
+    dev, in_dtype = cuda_index("x", x), x.dtype
+    B, H, T, d, K, w, b = _sizes(x, weight, bias, dev, True)
+    xp = check("x", x, x.shape, in_dtype, dev)
     s_shape = x.shape[:-2] + (K - 1, d)
-    if state is not None:
-        check("state", state, s_shape, in_dtype, dev)
+    sp = None if state is None else check("state", state, s_shape, in_dtype, dev)
     n = check_whole("lengths", lengths, (B,), torch.int32, dev)
-    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, in_dtype)
+    out_dtype = out_dtype_of(out_dtype, y, in_dtype)
+    mode = _mode(in_dtype, out_dtype, silu, y is None)
     with On(dev, stream, (x, weight, bias, state, lengths, y, state_T)) as s:
         if y is None:
-            make = torch.empty if lengths is None else torch.zeros
-            y = make(x.shape, dtype=out_dtype, device=dev)
-        else:
-            check("y", y, x.shape, out_dtype, dev)
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        yp = check("y", y, x.shape, out_dtype, dev)
         if state_T is None:
             state_T = torch.empty(s_shape, dtype=in_dtype, device=dev)
-        else:
-            check("state_T", state_T, s_shape, in_dtype, dev)
+        tp = check("state_T", state_T, s_shape, in_dtype, dev)
         o = _OUTER[x.dim()]
-        st = strides_of((x, o), (y, o), (s_shape if state is None else state, o), (state_T, o))
-        rc = _lib().ttt_conv_forward(
-            x.data_ptr(), w, b, None if state is None else state.data_ptr(), n, B, H, T, d, K,
-            _mode(in_dtype, out_dtype, silu), st, y.data_ptr(), state_T.data_ptr(), s)
+        st = strides_of(12, (x, o), (y, o), (s_shape if state is None else state, o), (state_T, o))
+        rc = _lib.ttt_conv_forward(xp, w, b, sp, n, B, H, T, d, K, mode, st, yp, tp, s)
     raise_for(rc, "ttt_conv_forward")
     return y, state_T
 
 
 def backward_workspace_bytes(B: int, H: int, T: int, d: int, K: int) -> int:
     """Bytes of device workspace ``ttt_conv_backward`` needs for these sizes."""
-    return int(_lib().ttt_conv_backward_workspace_bytes(B, H, T, d, K))
+    return int(_lib.ttt_conv_backward_workspace_bytes(B, H, T, d, K))
 
 
 def causal_conv_backward(x, weight, bias, dy, dstate_T=None, *, silu: bool = False, state=None,
@@ -110,34 +108,29 @@ def causal_conv_backward(x, weight, bias, dy, dstate_T=None, *, silu: bool = Fal
     ``workspace`` (optional): at least ``backward_workspace_bytes`` bytes, not shared by calls that
     overlap.
     """
-    dev, in_dtype = check_device("x", x), check_dtype("x", x)
-    B, H, T, d, K, channels, w, b = _sizes(x, weight, bias, dev, True)
-    check("x", x, x.shape, in_dtype, dev)
-    check("dy", dy, x.shape, check_dtype("dy", dy), dev)
+    dev, in_dtype = cuda_index("x", x), x.dtype
+    B, H, T, d, K, w, b = _sizes(x, weight, bias, dev, True)
+    xp = check("x", x, x.shape, in_dtype, dev)
+    gp = check_float("dy", dy, x.shape, dev)
     s_shape = x.shape[:-2] + (K - 1, d)
-    if state is not None:
-        check("state", state, s_shape, in_dtype, dev)
+    sp = None if state is None else check("state", state, s_shape, in_dtype, dev)
     ds_T = check_whole("dstate_T", dstate_T, s_shape, in_dtype, dev)
     n = check_whole("lengths", lengths, (B,), torch.int32, dev)
     o = _OUTER[x.dim()]
-    st = strides_of((x, o), (dy, o), (s_shape if state is None else state, o))
+    st = strides_of(9, (x, o), (dy, o), (s_shape if state is None else state, o))
     with On(dev, stream, (x, weight, bias, dy, dstate_T, state, lengths, workspace)) as s:
-        need = backward_workspace_bytes(B, H, T, d, K)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        check_whole("workspace", workspace, workspace.shape, workspace.dtype, dev)
-        out = dict(dx=torch.empty(x.shape, dtype=in_dtype, device=dev),
-                   dweight=torch.empty_like(weight),
-                   dbias=None if bias is None else torch.empty_like(bias),
-                   dstate=torch.empty(s_shape, dtype=in_dtype, device=dev))
-        rc = _lib().ttt_conv_backward(
-            x.data_ptr(), w, b, None if state is None else state.data_ptr(), n, B, H, T, d, K,
-            _mode(in_dtype, dy.dtype, silu), st, dy.data_ptr(), ds_T, out["dx"].data_ptr(),
-            out["dweight"].data_ptr(), None if bias is None else out["dbias"].data_ptr(),
-            out["dstate"].data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s)
+        workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(B, H, T, d, K), dev)
+        dx = torch.empty(x.shape, dtype=in_dtype, device=dev)
+        dstate = torch.empty(s_shape, dtype=in_dtype, device=dev)
+        dweight = torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        rc = _lib.ttt_conv_backward(xp, w, b, sp, n, B, H, T, d, K,
+                                    _mode(in_dtype, dy.dtype, silu, False), st, gp, ds_T,
+                                    dx.data_ptr(), dweight.data_ptr(),
+                                    None if bias is None else dbias.data_ptr(), dstate.data_ptr(),
+                                    wp, wn, s)
     raise_for(rc, "ttt_conv_backward")
-    return out
+    return dict(dx=dx, dweight=dweight, dbias=dbias, dstate=dstate)
 
 
 def causal_conv_step(x, weight, bias, state, *, silu: bool = False, active=None,
@@ -149,21 +142,19 @@ def causal_conv_step(x, weight, bias, state, *, silu: bool = False, active=None,
     PLACE; active: [B] uint8 or None, 0 = the row's state and y are left as they were (a y made here
     is 0 there). A chain of steps equals ``causal_conv``.
     """
-    dev, in_dtype = check_device("x", x), check_dtype("x", x)
-    B, H, _, d, K, channels, w, b = _sizes(x, weight, bias, dev, False)
-    check("x", x, x.shape, in_dtype, dev)
-    check("state", state, x.shape[:-1] + (K - 1, d), in_dtype, dev)
+    dev, in_dtype = cuda_index("x", x), x.dtype
+    B, H, _, d, K, w, b = _sizes(x, weight, bias, dev, False)
+    xp = check("x", x, x.shape, in_dtype, dev)
+    sp = check("state", state, x.shape[:-1] + (K - 1, d), in_dtype, dev)
     a = check_whole("active", active, (B,), torch.uint8, dev)
-    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, in_dtype)
+    out_dtype = out_dtype_of(out_dtype, y, in_dtype)
+    mode = _mode(in_dtype, out_dtype, silu, y is None)
     with On(dev, stream, (x, weight, bias, state, active, y)) as s:
         if y is None:
-            make = torch.empty if active is None else torch.zeros
-            y = make(x.shape, dtype=out_dtype, device=dev)
-        else:
-            check("y", y, x.shape, out_dtype, dev)
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        yp = check("y", y, x.shape, out_dtype, dev)
         o = (0, 1) if x.dim() == 3 else (0, 0)
-        st = strides_of((x, o), (y, o), (state, _OUTER[state.dim()]))
-        rc = _lib().ttt_conv_step(x.data_ptr(), w, b, state.data_ptr(), a, B, H, d, K,
-                                  _mode(in_dtype, out_dtype, silu), st, y.data_ptr(), s)
+        st = strides_of(7, (x, o), (y, o), (state, _OUTER[state.dim()]))
+        rc = _lib.ttt_conv_step(xp, w, b, sp, a, B, H, d, K, mode, st, yp, s)
     raise_for(rc, "ttt_conv_step")
     return y

@@ -52,7 +52,7 @@ using ttt::abi::misaligned_to;
 using ttt::abi::Span;
 using ttt::abi::Strided;
 
-constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_CONV_SILU;
+constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_CONV_SILU | TTT_CONV_PAD_ZERO;
 constexpr int kMaxGridY = 65535;
 
 enum Which { kForward, kBackward, kStep };
@@ -177,6 +177,7 @@ int ttt_conv_forward(const void* x, const float* weight, const float* bias, cons
   p.y = y; p.state_T = state_T;
   p.B = B; p.H = H; p.T = T; p.d = d;
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
+  p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
   p.tiles = T > 0 ? (int)(((long long)T + ttt::kConvRun - 1) / ttt::kConvRun) : 1;
   return dispatch<kForward>(p, K, mode, can_vec(kForward, mode, d, ts, ptrs, 4),
                             static_cast<cudaStream_t>(cuda_stream));
@@ -239,6 +240,7 @@ int ttt_conv_backward(const void* x, const float* weight, const float* bias, con
   p.part = static_cast<float*>(workspace);
   p.B = B; p.H = H; p.T = T; p.d = d;
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
+  p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
   const int rc =
       dispatch<kBackward>(p, K, mode, can_vec(kBackward, mode, d, ts, ptrs, 6), s);
   if (rc != TTT_OK) return rc;
@@ -275,6 +277,7 @@ int ttt_conv_step(const void* x, const float* weight, const float* bias, void* s
   p.x = x; p.weight = weight; p.bias = bias; p.active = active; p.y = y; p.state_T = state;
   p.B = B; p.H = H; p.T = 1; p.d = d;
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
+  p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
   return dispatch<kStep>(p, K, mode, can_vec(kStep, mode, d, ts, ptrs, 3),
                          static_cast<cudaStream_t>(cuda_stream));
 }

@@ -34,6 +34,7 @@ struct ConvParams {
   int vecs;             // vectors of VEC channels over all heads: H * d / VEC
   int tiles;            // runs of tokens (forward), blocks along the tokens (backward)
   int silu;
+  int pad_zero;         // y = 0 behind a length and in rows that are not active
 };
 
 template <typename T>
@@ -129,12 +130,18 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvParams p) {
         }
       }
     } else {
-      if (t0 >= len) continue;
+      if (t0 < len)
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-        load_vec<InT, VEC>(xp + (long long)(t0 - (K - 1) + j) * p.xs.t, win[j + 1]);
+        for (int j = 0; j < K - 1; ++j)
+          load_vec<InT, VEC>(xp + (long long)(t0 - (K - 1) + j) * p.xs.t, win[j + 1]);
     }
     OutT* yp = row_ptr<OutT>(p.y, p.ys, b, h, 0, c);
+    if (p.pad_zero) {
+      const float none[VEC] = {};
+      const int end = t0 + kConvRun < p.T ? t0 + kConvRun : p.T;
+      for (int t = len > t0 ? len : t0; t < end; ++t)
+        store_vec<OutT, VEC>(yp + (long long)t * p.ys.t, none);
+    }
     constexpr int NB = VEC == 8 ? 4 : 8;  // tokens loaded at a time
     for (int s = 0; s < kConvRun; s += NB) {
       const int ts = t0 + s;
@@ -336,8 +343,15 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
   float w[VEC][K];
   load_weights<VEC, K>(p.weight, cc, w);
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    if (p.active && !p.active[b]) continue;
     float win[K][VEC], out[VEC];
+    if (p.active && !p.active[b]) {
+      if (p.pad_zero) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+        store_vec<OutT, VEC>(row_ptr<OutT>(p.y, p.ys, b, h, 0, c), out);
+      }
+      continue;
+    }
     InT* st = row_ptr<InT>(p.state_T, p.ss, b, h, 0, c);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) load_vec<InT, VEC>(st + j * p.ss.t, win[j]);

@@ -15,16 +15,32 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 1 / x on the special-function unit (2^-23); 1 / inf = 0, a denormal x counts as 0.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 1 / (1 + exp(-x)) from one ex2 and one reciprocal, a few units in the last place
 // off; exp(-x) = inf gives 0.
 __device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.0f, 1.0f + ex2(-kLog2e * x));
+  return rcp(1.0f + ex2(-kLog2e * x));
 }
 
 // log(1 + exp(x)), accurate in the relative sense on both sides (a step size of
-// 1e-3 needs log1p: 1 + e would keep 4 of its digits).
+// 1e-3 needs log1p: 1 + e would keep 4 of its digits). With e = exp(-|x|) it is
+// max(x, 0) + log1p(e), and log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3:
+// 2 s P(s^2), P the degree-4 polynomial through atanh(s) / s at the Chebyshev nodes of
+// [0, 1/9] (4e-9 off). A third of log1pf's instructions.
 __device__ __forceinline__ float softplus(float x) {
-  return fmaxf(x, 0.0f) + log1pf(ex2(-kLog2e * fabsf(x)));
+  const float e = ex2(-kLog2e * fabsf(x));
+  const float s = e * rcp(2.0f + e), z = s * s;
+  float p = fmaf(0.140788892f, z, 0.139825789f);
+  p = fmaf(p, z, 0.200122976f);
+  p = fmaf(p, z, 0.333331608f);
+  p = fmaf(p, z, 1.0f);
+  return fmaf(2.0f * s, p, fmaxf(x, 0.0f));
 }
 
 // Load VEC consecutive elements, widened to fp32. VEC > 1 needs the address

@@ -1,5 +1,7 @@
 // C-ABI entry points of the selective state space scan (include/ttt_ssm.h):
 // argument checks, how far a prompt's tokens are split over CTAs, launches.
+#include <initializer_list>
+
 #include "ttt_ssm.h"
 #include "abi_util.h"
 #include "launch.h"
@@ -15,29 +17,34 @@ using ttt::abi::misaligned_to;
 using ttt::abi::Span;
 using ttt::abi::Strided;
 
-constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_SSM_SOFTPLUS;
+constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_SSM_SOFTPLUS | TTT_SSM_PAD_ZERO;
 constexpr int kMaxGridY = 65535;
+constexpr long long kMaxTokenStride = 1 << 24;  // 16 tokens of 4 bytes and a row of channels: 32 bits
 
 int check_sizes(int B, int T, int D, int G, int N, unsigned mode) {
   if (mode & ~kKnownModes) return TTT_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || D < 1 || G < 1 || N < 1 || D % G != 0) return TTT_ERR_INVALID_ARG;
   if (N != 8 && N != 16 && N != 32 && N != 64) return TTT_ERR_UNSUPPORTED;
-  if ((long long)D * N > 0x7fffffffLL || (long long)G * N > 0x7fffffffLL)
+  if (D > kMaxTokenStride || (long long)G * N > kMaxTokenStride || (long long)D * N > 0x7fffffffLL)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
-int threads_per_channel(int N) { return N / 4; }
-
-int channel_tiles(int D, int G, int N, int threads) {
-  const int ch = threads / threads_per_channel(N);
+int channel_tiles(int D, int G, int lanes, int threads) {
+  const int ch = threads / lanes;
   return (D / G + ch - 1) / ch;
 }
 
+// CTAs along the tokens for `ctas` pairs of a row and a channel tile. Each CTA of a split runs its
+// span nearly twice, so a split has to bring at least twice the SMs into play: none with
+// more than half an SM's worth of pairs (128 pairs, 4096 tokens, forward: 172 us whole, 248 us
+// in two), then up to two CTAs per SM (32 pairs: 174 us whole, 154 in two, 82 in four, 74 in
+// eight). A span keeps 8 tiles, so that the exchange stays small beside it.
 int split_for(long long ctas, int T, int sms) {
+  if (2 * ctas > sms) return 1;
   const int tiles = (T + ttt::kSsmTile - 1) / ttt::kSsmTile;
   int s = 1;
-  while (s < ttt::kSsmMaxSplit && ctas * s * 2 <= 4LL * sms && tiles >= 8 * s) s *= 2;
+  while (s < ttt::kSsmMaxSplit && ctas * s <= sms && tiles >= 16 * s) s *= 2;
   return s;
 }
 
@@ -50,7 +57,7 @@ template <typename Kernel>
 int launch_kernel(Kernel kernel, long long blocks, int split, int B, int threads, size_t smem,
                   const SsmParams& p, cudaStream_t s) {
   if (blocks * split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return TTT_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
@@ -67,13 +74,25 @@ int launch_kernel(Kernel kernel, long long blocks, int split, int B, int threads
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
+// Forward: P states a thread (N = 16: 4; with 2, more warps and more parts to add, 1.38 against 1.33 ms
+// for two prompts of 32768 tokens by 2048 channels).
+template <int N, int P, typename InT, int VEC>
+int launch_fwd_as(SsmParams p, cudaStream_t s) {
+  using S = ttt::SsmFwdShape<N, P, InT, VEC>;
+  p.tiles = (p.per_group + S::CH - 1) / S::CH;
+  const long long blocks = (long long)p.tiles * p.G;
+  p.split = split_for(blocks * p.B, p.T, sm_count());
+  constexpr size_t smem = sizeof(typename S::Smem);
+  return p.split > 1
+             ? launch_kernel(ttt::ssm_fwd_kernel<N, P, InT, VEC, true>, blocks, p.split, p.B, S::NT, smem, p, s)
+             : launch_kernel(ttt::ssm_fwd_kernel<N, P, InT, VEC, false>, blocks, 1, p.B, S::NT, smem, p, s);
+}
+
 template <int L, typename InT>
 int launch_fwd(const SsmParams& p, cudaStream_t s) {
-  using S = ttt::SsmFwdShape<L>;
-  const long long blocks = (long long)p.tiles * p.G;
-  return p.split > 1
-             ? launch_kernel(ttt::ssm_fwd_kernel<L, InT, true>, blocks, p.split, p.B, S::NT, 0, p, s)
-             : launch_kernel(ttt::ssm_fwd_kernel<L, InT, false>, blocks, 1, p.B, S::NT, 0, p, s);
+  constexpr int N = 4 * L;
+  constexpr int P = N <= 16 ? 4 : 8;
+  return p.vec ? launch_fwd_as<N, P, InT, 4>(p, s) : launch_fwd_as<N, P, InT, 1>(p, s);
 }
 
 template <int L, typename InT>
@@ -118,20 +137,21 @@ int dispatch(const SsmParams& p, int N, unsigned mode, cudaStream_t s) {
   return (mode & TTT_IN_BF16) ? dispatch_n<W, __nv_bfloat16>(p, N, s) : dispatch_n<W, float>(p, N, s);
 }
 
-// Strides of a prompt's tensors into p (null: contiguous).
-void set_strides(SsmParams& p, int T, int D, int G, int N, const long long* s) {
-  const long long tok = (long long)T * D, vec = (long long)T * G * N;
-  if (s) {
-    p.u_b = s[0]; p.u_t = s[1]; p.d_b = s[2]; p.d_t = s[3]; p.z_b = s[4]; p.z_t = s[5];
-    p.Bm_b = s[6]; p.Bm_t = s[7]; p.Bm_g = s[8]; p.Cm_b = s[9]; p.Cm_t = s[10]; p.Cm_g = s[11];
-    p.y_b = s[12]; p.y_t = s[13];
-  } else {
-    p.u_b = p.d_b = p.z_b = p.y_b = tok;
-    p.u_t = p.d_t = p.z_t = p.y_t = D;
-    p.Bm_b = p.Cm_b = vec;
-    p.Bm_t = p.Cm_t = (long long)G * N;
-    p.Bm_g = p.Cm_g = N;
+// Strides of a prompt's tensors into p (null: contiguous). False: a token stride
+// that is negative or too long for the kernels' arithmetic within a tile.
+bool set_strides(SsmParams& p, int T, int D, int G, int N, const long long* s) {
+  const long long tok = (long long)T * D, vec = (long long)T * G * N, gn = (long long)G * N;
+  const long long whole[14] = {tok, D, tok, D, tok, D, vec, gn, N, vec, gn, N, tok, D};
+  if (!s) s = whole;
+  p.u_b = s[0]; p.d_b = s[2]; p.z_b = s[4]; p.Bm_b = s[6]; p.Bm_g = s[8]; p.Cm_b = s[9];
+  p.Cm_g = s[11]; p.y_b = s[12];
+  const long long t[6] = {s[1], s[3], s[5], s[7], s[10], s[13]};
+  int* to[6] = {&p.u_t, &p.d_t, &p.z_t, &p.Bm_t, &p.Cm_t, &p.y_t};
+  for (int i = 0; i < 6; ++i) {
+    if (t[i] < 0 || t[i] > kMaxTokenStride) return false;
+    *to[i] = (int)t[i];
   }
+  return true;
 }
 
 struct Tensors {
@@ -148,9 +168,20 @@ Tensors tensors(const SsmParams& p, int B, int T, int D, int G, int N, size_t ie
           {{B, T, G}, {p.Cm_b, p.Cm_t, p.Cm_g}, N, ie},   {{B, T, 1}, {p.y_b, p.y_t, 0}, D, oe}};
 }
 
+// Can every row of channels and of Bm and Cm be read and written in packs of 4?
+bool packs_of_4(const SsmParams& p, std::initializer_list<const void*> in, size_t ie, const void* y,
+                size_t oe) {
+  for (const void* q : in)
+    if (misaligned_to(q, 4 * ie)) return false;
+  long long all = p.u_b | p.u_t | p.d_b | p.d_t | p.Bm_b | p.Bm_t | p.Bm_g | p.Cm_b | p.Cm_t |
+                  p.Cm_g | p.y_b | p.y_t | p.per_group;
+  if (p.z) all |= p.z_b | p.z_t;
+  return !misaligned_to(y, 4 * oe) && all % 4 == 0;
+}
+
 size_t par_floats(int B, int D, int N) { return (size_t)B * ttt::kSsmMaxSplit * D * (N + 2); }
 size_t bc_floats(int B, int T, int D, int G, int N) {
-  return (size_t)channel_tiles(D, G, N, 256) * B * T * G * 2 * N;
+  return (size_t)channel_tiles(D, G, N / 4, 256) * B * T * G * 2 * N;
 }
 
 }  // namespace
@@ -172,7 +203,7 @@ int ttt_ssm_forward(const void* u, const void* delta, const float* A, const void
       misaligned_to(Bm, ie) || misaligned_to(Cm, ie) || misaligned_to(y, oe))
     return TTT_ERR_INVALID_ARG;
   SsmParams p{};
-  set_strides(p, T, D, G, N, strides);
+  if (!set_strides(p, T, D, G, N, strides)) return TTT_ERR_INVALID_ARG;
   const Tensors ts = tensors(p, B, T, D, G, N, ie, oe);
   if (ts.negative() || ts.y.self_overlap()) return TTT_ERR_INVALID_ARG;
   const size_t state = (size_t)B * D * N * 4;
@@ -190,10 +221,10 @@ int ttt_ssm_forward(const void* u, const void* delta, const float* A, const void
   p.y = y; p.h_T = h_T; p.h_chunks = h_chunks;
   p.B = B; p.T = T; p.D = D; p.G = G;
   p.per_group = D / G;
-  p.tiles = channel_tiles(D, G, N, 128);
-  p.split = split_for((long long)p.tiles * G * B, T, sm_count());
   p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
   p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  p.pad_zero = (mode & TTT_SSM_PAD_ZERO) ? 1 : 0;
+  p.vec = packs_of_4(p, {u, delta, z, Bm, Cm}, ie, y, oe);
   return dispatch<kForward>(p, N, mode, static_cast<cudaStream_t>(cuda_stream));
 }
 
@@ -228,7 +259,7 @@ int ttt_ssm_backward(const void* u, const void* delta, const float* A, const voi
   const size_t need = ttt_ssm_backward_workspace_bytes(B, T, D, G, N);
   if (workspace_bytes < need) return TTT_ERR_INVALID_ARG;
   SsmParams p{};
-  set_strides(p, T, D, G, N, strides);
+  if (!set_strides(p, T, D, G, N, strides)) return TTT_ERR_INVALID_ARG;
   const Tensors ts = tensors(p, B, T, D, G, N, ie, oe);
   if (ts.negative()) return TTT_ERR_INVALID_ARG;
   const size_t state = (size_t)B * D * N * 4, par = (size_t)D * N * 4;
@@ -260,10 +291,11 @@ int ttt_ssm_backward(const void* u, const void* delta, const float* A, const voi
   p.part_par = p.part_bc + bc_floats(B, T, D, G, N);
   p.B = B; p.T = T; p.D = D; p.G = G;
   p.per_group = D / G;
-  p.tiles = channel_tiles(D, G, N, 256);
+  p.tiles = channel_tiles(D, G, N / 4, 256);
   p.split = split_for((long long)p.tiles * G * B, T, sm_count());
   p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
   p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  p.pad_zero = (mode & TTT_SSM_PAD_ZERO) ? 1 : 0;
   const size_t bc = (size_t)B * T * G * 2 * N;
   const size_t bc_blocks = (bc / 4 + 255) / 256;
   if (bc_blocks > 0x7fffffffULL || (long long)B * p.split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
@@ -300,9 +332,9 @@ int ttt_ssm_step(const void* u, const void* delta, const float* A, const void* B
   if (strides) {
     const long long full[14] = {strides[0], 0, strides[1], 0, strides[2], 0, strides[3], 0,
                                 strides[4], strides[5], 0, strides[6], strides[7], 0};
-    set_strides(p, 1, D, G, N, full);
+    if (!set_strides(p, 1, D, G, N, full)) return TTT_ERR_INVALID_ARG;
   } else {
-    set_strides(p, 1, D, G, N, nullptr);
+    if (!set_strides(p, 1, D, G, N, nullptr)) return TTT_ERR_INVALID_ARG;
   }
   const Tensors ts = tensors(p, B, 1, D, G, N, ie, oe);
   if (ts.negative() || ts.y.self_overlap()) return TTT_ERR_INVALID_ARG;
@@ -319,7 +351,9 @@ int ttt_ssm_step(const void* u, const void* delta, const float* A, const void* B
   p.per_group = D / G;
   p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
   p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
+  p.pad_zero = (mode & TTT_SSM_PAD_ZERO) ? 1 : 0;
   return dispatch<kStep>(p, N, mode, static_cast<cudaStream_t>(cuda_stream));
 }
 
 }  // extern "C"
+

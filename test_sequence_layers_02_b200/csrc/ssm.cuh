@@ -3,9 +3,13 @@
 //
 // Work: one exponential, one multiply and two multiply-adds for each of the N
 // states of every (token, channel), against four 2- or 4-byte elements of
-// traffic. At N = 16 the special-function units (16 lanes per clock and SM) bind:
+// traffic. At N = 16 the special-function units (16 lanes per clock and SM) bind first:
 // (N + 4) / 16 clocks per (token, channel) with the softplus and the gate counted,
-// where HBM would take a quarter of that in bf16.
+// where HBM would take a quarter of that in bf16. Measured, bf16, N = 16: two prompts of 32768
+// tokens by 2048 channels 1.33 ms (0.59 ms at that bound, with 128 CTAs on 148 SMs); 16 of 2048 by
+// 1536 0.41 ms (0.22). What is left is the latency of the loop, about 80 clocks a token for
+// a warp of the recurrence that shares its scheduler with staging and output, 57 alone; without
+// its exponentials it still takes 69.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -25,14 +29,16 @@ struct SsmParams {
   void* y;
   float* h_T;               // [B, D, N] (step: in place)
   float* h_chunks;          // [B, ceil(T / 16), D, N] or null
-  long long u_b, u_t, d_b, d_t, z_b, z_t;        // element strides: rows, tokens
-  long long Bm_b, Bm_t, Bm_g, Cm_b, Cm_t, Cm_g;  // rows, tokens, groups
-  long long y_b, y_t;
+  // Element strides: batch rows, groups, tokens. The bytes of 16 tokens fit an int (checked).
+  long long u_b, d_b, z_b, Bm_b, Bm_g, Cm_b, Cm_g, y_b;
+  int u_t, d_t, z_t, Bm_t, Cm_t, y_t;
   int B, T, D, G;
   int per_group;            // D / G
   int tiles;                // channel tiles per group
+  int vec;                  // rows can be read and written in packs of 4
   int split;                // CTAs along the tokens (one cluster)
   int softplus, out_bf16;
+  int pad_zero;             // y = 0 behind a length and in rows that are not active
   // backward
   const void* dy;           // strides y_b, y_t
   const float* dh_T;        // or null
@@ -113,19 +119,115 @@ __device__ __forceinline__ void store_state(float* p, const State4& s) {
   *reinterpret_cast<float4*>(p) = make_float4(s.lo.x, s.lo.y, s.hi.x, s.hi.y);
 }
 
-// L = N / 4 lanes hold one channel, four states each; a CTA of 128 threads has
-// 128 / L channels and walks tiles of 16 tokens. The step sizes are worked out once
-// for each (token, channel) as a tile is staged in shared memory, the next tile's
-// inputs are on their way to registers meanwhile, and the L partial sums of an
-// output are added for L tokens at once (L - 1 shuffles in place of L log2 L).
-template <int L>
+// P states of one channel in a lane, as pairs for the paired fp32 instructions.
+template <int P>
+struct States {
+  float2 v[P / 2];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) v[i] = dup2(0.f);
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (P == 2) {
+      v[0] = *reinterpret_cast<const float2*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P / 4; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(p)[i];
+        v[2 * i] = make_float2(x.x, x.y);
+        v[2 * i + 1] = make_float2(x.z, x.w);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    if constexpr (P == 2) {
+      *reinterpret_cast<float2*>(p) = v[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < P / 4; ++i)
+        reinterpret_cast<float4*>(p)[i] =
+            make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+    }
+  }
+};
+
+// VEC neighbouring elements of a row as they are in memory, in as few registers.
+template <typename T, int VEC>
+struct Pack;
+template <>
+struct Pack<float, 1> {
+  float v;
+  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = v; }
+};
+template <>
+struct Pack<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void widen(float (&o)[4]) const {
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+  unsigned short v;
+  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
+};
+template <>
+struct Pack<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void widen(float (&o)[4]) const {
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+
+// Copy BYTES (4, 8 or 16) to shared memory without a register; `have` false: zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool have) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
+               "r"(have ? BYTES : 0) : "memory");
+}
+
+// A CTA has 32 CW channels. A warp of the recurrence holds P of the N states of 32 channels, a
+// channel a lane, so that the tile's Bm and Cm are the same address for all its lanes; N / P
+// warps share a channel and leave their parts of its output in shared memory. Two more sets
+// of four warps do everything around the recurrence once for each (token, channel), VEC channels
+// a thread: one stages a tile of 16 tokens in shared memory, with its step sizes and gates, one
+// adds the parts and writes out. One barrier a tile: between two of them the first
+// run tile k, the second stage tile k + 1 in the other half of shared memory, the third write
+// out tile k - 1. The loads of the tiles behind that are on their way: RING tiles in packs of
+// 4 elements, which go to a ring in shared memory by asynchronous copies (a thread
+// reads back what it copied, so the ring needs no barrier), or two tiles of single
+// elements in registers where rows do not allow packs. A lone CTA on an SM lives by that
+// depth: a tile takes it half a microsecond, a load from HBM more than that.
+template <int N, int P, typename InT, int VEC>
 struct SsmFwdShape {
-  static constexpr int NT = 128;
-  static constexpr int N = 4 * L;
-  static constexpr int CH = NT / L;             // channels
-  static constexpr int IT = kSsmTile / L;       // (token, channel) items per thread and tile
-  static constexpr int NBC = kSsmTile * N / NT; // entries of Bm (and Cm) per thread and tile
-  static constexpr int YS = CH + 32 / L;        // row of the output tile: no bank conflicts
+  static constexpr int L = N / P;               // warps that share a channel
+  static constexpr int CW = L < 4 ? 4 / L : 1;  // blocks of 32 channels
+  static constexpr int CH = 32 * CW;
+  static constexpr int RT = CH * L;             // threads of the recurrence
+  static constexpr int HT = 128;                // threads that stage, and threads that write out
+  static constexpr int NT = RT + 2 * HT;
+  static constexpr int QUADS = CH / VEC;        // items of a token
+  static constexpr int TS = HT / QUADS;         // tokens between a helper's items
+  static constexpr int IT = kSsmTile / TS;      // items per helper and tile
+  static constexpr int BCQ = kSsmTile * N / VEC;             // packs of Bm (and Cm) in a tile
+  static constexpr int NBC = (BCQ + HT - 1) / HT;            // ... per helper
+  static constexpr int GROUP = 2;               // tokens whose exponentials are taken at once
+  static constexpr int RING = VEC == 1 ? 0 : 16 / (int)sizeof(InT);
+  static_assert(HT % QUADS == 0 && kSsmTile % TS == 0, "whole items");
+  static_assert(BCQ % HT == 0 || BCQ < HT, "whole packs");
+  struct Smem {
+    alignas(16) float2 dt[2][kSsmTile][CH];     // dt, dt u
+    alignas(16) float2 gate[4][kSsmTile][CH];   // SiLU(z), SiLU(z) skip u: read two tiles later
+    alignas(16) float B[2][kSsmTile][N];
+    alignas(16) float C[2][kSsmTile][N];
+    alignas(16) float y[2][kSsmTile][L][CH];    // the warps' parts of the read-out
+    struct Slot {
+      Pack<InT, VEC> u[IT][HT], d[IT][HT], z[IT][HT], B[NBC][HT], C[NBC][HT];
+    } ring[RING > 0 ? RING : 1];
+  };
 };
 
 // With SPLIT, a cluster of p.split CTAs shares the tokens of a (row, channel tile) when rows and
@@ -133,16 +235,19 @@ struct SsmFwdShape {
 // for its end state and decay, the cluster exchanges those through distributed
 // shared memory, and each runs its span again from the state it now knows. That is
 // up to twice the exponentials, over `split` times the CTAs.
-template <int L, typename InT, bool SPLIT>
-__global__ void __launch_bounds__(128) ssm_fwd_kernel(const SsmParams p) {
-  using S = SsmFwdShape<L>;
-  constexpr int N = S::N, CH = S::CH, IT = S::IT;
-  __shared__ float2 s_dt[kSsmTile][CH];  // dt, dt u
-  __shared__ __align__(16) float s_B[kSsmTile][N], s_C[kSsmTile][N];
-  __shared__ float s_y[kSsmTile][S::YS];
-  __shared__ float4 s_end[SPLIT ? S::NT : 1], s_decay[SPLIT ? S::NT : 1];
+template <int N, int P, typename InT, int VEC, bool SPLIT>
+__global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 1) ssm_fwd_kernel(const SsmParams p) {
+  using S = SsmFwdShape<N, P, InT, VEC>;
+  constexpr int L = S::L, CH = S::CH, IT = S::IT, TS = S::TS, RT = S::RT, HT = S::HT;
+  constexpr int NBC = S::NBC, QUADS = S::QUADS, RING = S::RING;
+  using In = Pack<InT, VEC>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(smem_raw);
+  __shared__ float2 s_end[SPLIT ? P / 2 : 1][SPLIT ? RT : 1], s_decay[SPLIT ? P / 2 : 1][SPLIT ? RT : 1];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  enum { kRecur, kStage, kWrite };
+  const int role = threadIdx.x < RT ? kRecur : threadIdx.x < RT + HT ? kStage : kWrite;
+  const int tid = role == kRecur ? threadIdx.x : (threadIdx.x - RT) % HT;  // within the role
   const int rank = SPLIT ? blockIdx.x % p.split : 0;
   const int tile = SPLIT ? blockIdx.x / p.split : blockIdx.x;
   const int g = tile / p.tiles;
@@ -150,20 +255,27 @@ __global__ void __launch_bounds__(128) ssm_fwd_kernel(const SsmParams p) {
   const int c0 = g * p.per_group + in_group;
   const int nch = min(CH, p.per_group - in_group);
 
-  // as part of a channel's lanes
-  const int my_ch = warp * (32 / L) + lane / L;
-  const int n0 = (lane % L) * 4;
-  const bool on = my_ch < nch;
+  // the recurrence: states n0 .. n0 + P - 1 of channel my_ch
+  const int part = (tid >> 5) % L;
+  const int my_ch = (tid >> 5) / L * 32 + (tid & 31);
+  const int n0 = part * P;
+  const bool on = role == kRecur && my_ch < nch;
   const size_t par = (size_t)(c0 + (on ? my_ch : 0)) * N + n0;
-  State4 A = load_state(p.A + par);
-  A.lo.x *= kLog2e; A.lo.y *= kLog2e; A.hi.x *= kLog2e; A.hi.y *= kLog2e;
+  States<P> A;
+  A.load(p.A + par);
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) A.v[i] = __fmul2_rn(A.v[i], dup2(kLog2e));
 
-  // as the owner of (token, channel) items: tokens it + L i of channel ic
-  const int ic = tid % CH, it = tid / CH;
+  // the others: tokens it + TS i of channels ic .. ic + VEC - 1
+  const int ic = tid % QUADS * VEC, it = tid / QUADS;
   const bool i_on = ic < nch;
   const int icc = c0 + (i_on ? ic : 0);
-  const float bias = p.delta_bias ? p.delta_bias[icc] : 0.f;
-  const float skip = p.skip ? p.skip[icc] : 0.f;
+  float bias[VEC], skip[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) {
+    bias[q] = p.delta_bias ? p.delta_bias[icc + q] : 0.f;
+    skip[q] = p.skip ? p.skip[icc + q] : 0.f;
+  }
 
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int len = ssm_length(p.lengths, b, p.T);
@@ -171,139 +283,356 @@ __global__ void __launch_bounds__(128) ssm_fwd_kernel(const SsmParams p) {
     const int per = SPLIT ? (n_tiles + p.split - 1) / p.split : n_tiles;
     const int first = min(n_tiles, rank * per), last = min(n_tiles, first + per);
 
-    const InT* up = static_cast<const InT*>(p.u) + b * p.u_b + icc;
-    const InT* dp = static_cast<const InT*>(p.delta) + b * p.d_b + icc;
-    const InT* zp = static_cast<const InT*>(p.z) + b * p.z_b + icc;
-    const InT* Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g;
-    const InT* Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g;
-
-    InT ru[IT], rd[IT], rz[IT], rB[S::NBC], rC[S::NBC];
-    auto fetch = [&](int k, bool all) {
+    // ---- around the recurrence ----
+    // Running pointers to a helper's items and packs of the tile to be fetched next.
+    const InT *up, *dp, *zp, *Bp, *Cp;
+    const bool bc_on = S::BCQ % HT == 0 || tid < S::BCQ;
+    constexpr int BROW = N / VEC;          // packs of a token
+    constexpr int BS = HT / BROW;          // tokens between a helper's packs
+    const int bt = tid / BROW, bn = tid % BROW * VEC;
+    struct Regs {
+      In u[IT], d[IT], z[IT], B[NBC], C[NBC];
+    };
+    auto advance = [&](bool all) {
+      up += kSsmTile * p.u_t;
+      dp += kSsmTile * p.d_t;
+      Bp += kSsmTile * p.Bm_t;
+      if (all) {
+        zp += kSsmTile * p.z_t;
+        Cp += kSsmTile * p.Cm_t;
+      }
+    };
+    // The inputs of tile k, in order, to registers (0 behind the length). `all`: those of the
+    // read-out too.
+    auto fetch = [&](Regs& r, int k, bool all) {
+      auto at = [](const InT* q) { return *reinterpret_cast<const In*>(q); };
+      const int left = len - k * kSsmTile;
+      const In none = {};
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int t = k * kSsmTile + it + L * i;
-        const bool have = i_on && t < len;
-        ru[i] = have ? up[t * p.u_t] : from_f32<InT>(0.f);
-        rd[i] = have ? dp[t * p.d_t] : from_f32<InT>(0.f);
-        if (all && p.z) rz[i] = have ? zp[t * p.z_t] : from_f32<InT>(0.f);
+        r.u[i] = r.d[i] = r.z[i] = none;
+        if (it + TS * i < left) {
+          r.u[i] = at(up + TS * i * p.u_t);
+          r.d[i] = at(dp + TS * i * p.d_t);
+          if (all && p.z) r.z[i] = at(zp + TS * i * p.z_t);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < S::NBC; ++j) {
-        const int e = tid + S::NT * j;
-        const int t = k * kSsmTile + e / N;
-        rB[j] = t < len ? Bp[t * p.Bm_t + e % N] : from_f32<InT>(0.f);
-        if (all) rC[j] = t < len ? Cp[t * p.Cm_t + e % N] : from_f32<InT>(0.f);
+      for (int j = 0; j < NBC; ++j) {
+        r.B[j] = r.C[j] = none;
+        if (bc_on && bt + BS * j < left) {
+          r.B[j] = at(Bp + BS * j * p.Bm_t);
+          if (all) r.C[j] = at(Cp + BS * j * p.Cm_t);
+        }
+      }
+      advance(all);
+    };
+    // The same to the ring (one group of copies a tile, also an empty one behind the last) ...
+    auto send = [&](int k, bool all) {
+      if (k < last) {
+        typename S::Smem::Slot& r = sm.ring[k % (RING > 0 ? RING : 1)];
+        const int left = len - k * kSsmTile;
+        constexpr int W = sizeof(In) < 4 ? 4 : sizeof(In);  // (single bf16 have no ring)
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const bool have = it + TS * i < left;
+          copy_async<W>(&r.u[i][tid], have ? up + TS * i * p.u_t : up, have);
+          copy_async<W>(&r.d[i][tid], have ? dp + TS * i * p.d_t : dp, have);
+          if (all && p.z) copy_async<W>(&r.z[i][tid], have ? zp + TS * i * p.z_t : zp, have);
+        }
+        if (bc_on) {
+#pragma unroll
+          for (int j = 0; j < NBC; ++j) {
+            const bool have = bt + BS * j < left;
+            copy_async<W>(&r.B[j][tid], have ? Bp + BS * j * p.Bm_t : Bp, have);
+            if (all) copy_async<W>(&r.C[j][tid], have ? Cp + BS * j * p.Cm_t : Cp, have);
+          }
+        }
+        advance(all);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // ... and from the ring: the oldest of the RING groups under way.
+    auto receive = [&](Regs& r, int k, bool all) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(RING > 0 ? RING - 1 : 0) : "memory");
+      const typename S::Smem::Slot& f = sm.ring[k % (RING > 0 ? RING : 1)];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        r.u[i] = f.u[i][tid];
+        r.d[i] = f.d[i][tid];
+        if (all && p.z) r.z[i] = f.z[i][tid];
+      }
+      if (bc_on) {
+#pragma unroll
+        for (int j = 0; j < NBC; ++j) {
+          r.B[j] = f.B[j][tid];
+          if (all) r.C[j] = f.C[j][tid];
+        }
       }
     };
     // dt = 0 behind the length: there the state neither decays nor takes anything
-    auto stage = [&](int k, bool all) {
+    auto stage = [&](const Regs& r, int k, bool all) {
+      const int h = k & 1;
+      const int left = len - k * kSsmTile;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int t = it + L * i;
-        const float x = to_f32(rd[i]) + bias;
-        float dt = p.softplus ? softplus(x) : x;
-        if (k * kSsmTile + t >= len || !i_on) dt = 0.f;
-        s_dt[t][ic] = make_float2(dt, dt * to_f32(ru[i]));
-      }
+        const int t = it + TS * i;
+        float dt[VEC], u[VEC];
+        r.d[i].widen(dt);
+        r.u[i].widen(u);
 #pragma unroll
-      for (int j = 0; j < S::NBC; ++j) {
-        const int e = tid + S::NT * j;
-        (&s_B[0][0])[e] = to_f32(rB[j]);
-        if (all) (&s_C[0][0])[e] = to_f32(rC[j]);
+        for (int q = 0; q < VEC; ++q) dt[q] += bias[q];
+        if (p.softplus) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) dt[q] = softplus(dt[q]);
+        }
+        if (t >= left) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) dt[q] = 0.f;
+        }
+        if constexpr (VEC == 1) {
+          sm.dt[h][t][ic] = make_float2(dt[0], dt[0] * u[0]);
+        } else {
+          float4* o = reinterpret_cast<float4*>(&sm.dt[h][t][ic]);
+#pragma unroll
+          for (int q = 0; q < VEC; q += 2)
+            o[q / 2] = make_float4(dt[q], dt[q] * u[q], dt[q + 1], dt[q + 1] * u[q + 1]);
+        }
+        if (all) {
+          float f[VEC];
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) f[q] = 1.f;
+          if (p.z) {
+            r.z[i].widen(f);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) f[q] *= sigmoid_fast(f[q]);
+          }
+          if constexpr (VEC == 1) {
+            sm.gate[k & 3][t][ic] = make_float2(f[0], f[0] * (skip[0] * u[0]));
+          } else {
+            float4* o = reinterpret_cast<float4*>(&sm.gate[k & 3][t][ic]);
+#pragma unroll
+            for (int q = 0; q < VEC; q += 2)
+              o[q / 2] = make_float4(f[q], f[q] * (skip[q] * u[q]), f[q + 1],
+                                     f[q + 1] * (skip[q + 1] * u[q + 1]));
+          }
+        }
+      }
+      if (bc_on) {
+#pragma unroll
+        for (int j = 0; j < NBC; ++j) {
+          float v[VEC];
+          r.B[j].widen(v);
+          store_vec<float, VEC>(&sm.B[h][bt + BS * j][bn], v);
+          if (all) {
+            r.C[j].widen(v);
+            store_vec<float, VEC>(&sm.C[h][bt + BS * j][bn], v);
+          }
+        }
       }
     };
+    __nv_bfloat16* y16;
+    float* y32;
+    // The outputs of tile k, from the warps' parts.
+    auto write_out = [&](int k) {
+      const int h = k & 1;
+      const int left = i_on ? len - k * kSsmTile : 0;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int t = it + TS * i;
+        float r[VEC];
+        load_vec<float, VEC>(&sm.y[h][t][0][ic], r);
+#pragma unroll
+        for (int j = 1; j < L; ++j) {
+          float v[VEC];
+          load_vec<float, VEC>(&sm.y[h][t][j][ic], v);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) r[q] += v[q];
+        }
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          const float2 f = sm.gate[k & 3][t][ic + q];
+          r[q] = fmaf(f.x, r[q], f.y);
+        }
+        if (t < left) {
+          if (p.out_bf16)
+            store_vec<__nv_bfloat16, VEC>(y16 + TS * i * p.y_t, r);
+          else
+            store_vec<float, VEC>(y32 + TS * i * p.y_t, r);
+        }
+      }
+      y16 += kSsmTile * p.y_t;
+      y32 += kSsmTile * p.y_t;
+    };
+    // A pass over the tiles; the roles meet at one barrier a tile (and, with the read-out, one behind
+    // the last): between two of them tile k is run, k + 1 staged and k - 1 written out.
+    auto stage_all = [&](bool all) {
+      const long long t0 = (long long)first * kSsmTile + it, e0 = (long long)first * kSsmTile + bt;
+      up = static_cast<const InT*>(p.u) + b * p.u_b + t0 * p.u_t + icc;
+      dp = static_cast<const InT*>(p.delta) + b * p.d_b + t0 * p.d_t + icc;
+      zp = static_cast<const InT*>(p.z) + b * p.z_b + t0 * p.z_t + icc;
+      Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g + e0 * p.Bm_t + bn;
+      Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g + e0 * p.Cm_t + bn;
+      if constexpr (RING > 0) {
+        Regs r;
+        for (int j = 0; j < RING; ++j) send(first + j, all);
+        receive(r, first, all);
+        stage(r, first, all);
+        send(first + RING, all);
+        for (int k = first; k < last; ++k) {
+          __syncthreads();
+          if (k + 1 < last) {
+            receive(r, k + 1, all);
+            stage(r, k + 1, all);
+            send(k + 1 + RING, all);
+          }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      } else {
+        Regs sets[2];
+        fetch(sets[0], first, all);
+        if (first + 1 < last) fetch(sets[1], first + 1, all);
+        stage(sets[0], first, all);
+        if (first + 2 < last) fetch(sets[0], first + 2, all);
+        for (int k0 = first; k0 < last; k0 += 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = k0 + j;
+            if (k >= last) break;
+            __syncthreads();
+            if (k + 1 < last) {
+              stage(sets[j ^ 1], k + 1, all);
+              if (k + 3 < last) fetch(sets[j ^ 1], k + 3, all);
+            }
+          }
+        }
+      }
+      if (all) __syncthreads();
+    };
+    auto write_all = [&]() {
+      const long long t0 = (long long)first * kSsmTile + it;
+      y16 = static_cast<__nv_bfloat16*>(p.y) + b * p.y_b + t0 * p.y_t + icc;
+      y32 = static_cast<float*>(p.y) + b * p.y_b + t0 * p.y_t + icc;
+      for (int k = first; k < last; ++k) {
+        __syncthreads();
+        if (k > first) write_out(k - 1);
+      }
+      __syncthreads();
+      write_out(last - 1);
+    };
 
-    State4 h = {dup2(0.f), dup2(0.f)};
+    // ---- the recurrence ----
+    States<P> h;
+    h.zero();
     const size_t hrow = (size_t)b * p.D * N + par;
+    float sum_dt = 0.f;
+    // Tile k; `read`: with the read-out. The exponentials of the next GROUP tokens stand before
+    // the chain of these in the program, so that the two overlap.
+    auto run = [&](int k, bool read) {
+      constexpr int GROUP = S::GROUP;
+      const int half = k & 1;
+      States<P> a[2][GROUP], x[2][GROUP], c[2][GROUP];
+      auto prepare = [&](int t0, States<P>* ga, States<P>* gx, States<P>* gc) {
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+          const float2 d = sm.dt[half][t0 + j][my_ch];
+          States<P> Bv;
+          Bv.load(&sm.B[half][t0 + j][n0]);
+          if (read) gc[j].load(&sm.C[half][t0 + j][n0]);
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) {
+            ga[j].v[i] = ex2_2(__fmul2_rn(dup2(d.x), A.v[i]));
+            gx[j].v[i] = __fmul2_rn(dup2(d.y), Bv.v[i]);
+          }
+          if (!read) sum_dt += d.x;
+        }
+      };
+      prepare(0, a[0], x[0], c[0]);
+#pragma unroll
+      for (int t0 = 0; t0 < kSsmTile; t0 += GROUP) {
+        const int cur = (t0 / GROUP) & 1;
+        if (t0 + GROUP < kSsmTile) prepare(t0 + GROUP, a[cur ^ 1], x[cur ^ 1], c[cur ^ 1]);
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+          float2 s;
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) {
+            h.v[i] = __ffma2_rn(a[cur][j].v[i], h.v[i], x[cur][j].v[i]);
+            if (read)
+              s = i == 0 ? __fmul2_rn(c[cur][j].v[i], h.v[i])
+                         : __ffma2_rn(c[cur][j].v[i], h.v[i], s);
+          }
+          if (read) sm.y[half][t0 + j][part][my_ch] = s.x + s.y;
+        }
+      }
+    };
 
     if constexpr (SPLIT) {
       namespace cg = cooperative_groups;
       cg::cluster_group cluster = cg::this_cluster();
-      float sum_dt = 0.f;
-      if (rank + 1 < p.split) {
-        if (first < last) fetch(first, false);
-        for (int k = first; k < last; ++k) {
-          stage(k, false);
-          __syncthreads();
-          if (k + 1 < last) fetch(k + 1, false);
-#pragma unroll
-          for (int t = 0; t < kSsmTile; ++t) {
-            const float2 d = s_dt[t][my_ch];
-            const State4 Bv = load_state(&s_B[t][n0]);
-            const float2 dt = dup2(d.x), dtu = dup2(d.y);
-            h.lo = __ffma2_rn(ex2_2(__fmul2_rn(dt, A.lo)), h.lo, __fmul2_rn(dtu, Bv.lo));
-            h.hi = __ffma2_rn(ex2_2(__fmul2_rn(dt, A.hi)), h.hi, __fmul2_rn(dtu, Bv.hi));
-            sum_dt += d.x;
+      if (rank + 1 < p.split && first < last) {
+        if (role == kStage) {
+          stage_all(false);
+        } else {
+          for (int k = first; k < last; ++k) {
+            __syncthreads();
+            if (role == kRecur) run(k, false);
           }
-          __syncthreads();
         }
       }
-      const float2 lo = ex2_2(__fmul2_rn(dup2(sum_dt), A.lo));
-      const float2 hi = ex2_2(__fmul2_rn(dup2(sum_dt), A.hi));
-      s_end[tid] = make_float4(h.lo.x, h.lo.y, h.hi.x, h.hi.y);
-      s_decay[tid] = make_float4(lo.x, lo.y, hi.x, hi.y);
-      h = p.h0 ? load_state(p.h0 + hrow) : State4{dup2(0.f), dup2(0.f)};
+      if (role == kRecur) {
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          s_end[i][tid] = h.v[i];
+          s_decay[i][tid] = ex2_2(__fmul2_rn(dup2(sum_dt), A.v[i]));
+        }
+        h.zero();
+        if (p.h0) h.load(p.h0 + hrow);
+      }
       cluster.sync();
-      for (int r = 0; r < rank; ++r) {
-        const float4 e = *cluster.map_shared_rank(&s_end[tid], r);
-        const float4 a = *cluster.map_shared_rank(&s_decay[tid], r);
-        h.lo = __ffma2_rn(make_float2(a.x, a.y), h.lo, make_float2(e.x, e.y));
-        h.hi = __ffma2_rn(make_float2(a.z, a.w), h.hi, make_float2(e.z, e.w));
+      if (role == kRecur) {
+        for (int r = 0; r < rank; ++r) {
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i)
+            h.v[i] = __ffma2_rn(*cluster.map_shared_rank(&s_decay[i][tid], r), h.v[i],
+                                *cluster.map_shared_rank(&s_end[i][tid], r));
+        }
       }
       cluster.sync();  // nobody writes or leaves while its shared memory is read
     } else {
-      if (p.h0) h = load_state(p.h0 + hrow);
+      if (role == kRecur && p.h0) h.load(p.h0 + hrow);
     }
 
-    float* chunk = p.h_chunks;
-    if (chunk) chunk += ((size_t)b * ((p.T + kSsmTile - 1) / kSsmTile) + first) * p.D * N + par;
-    if (first < last) fetch(first, true);
-    for (int k = first; k < last; ++k) {
-      stage(k, true);
-      float cu[IT], cz[IT];
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        cu[i] = to_f32(ru[i]);
-        cz[i] = p.z ? to_f32(rz[i]) : 0.f;
-      }
-      __syncthreads();
-      if (k + 1 < last) fetch(k + 1, true);
-      if (chunk) {
-        if (on) store_state(chunk, h);
-        chunk += (size_t)p.D * N;
-      }
-#pragma unroll
-      for (int t0 = 0; t0 < kSsmTile; t0 += L) {
-        float v[L];
-#pragma unroll
-        for (int q = 0; q < L; ++q) {
-          const float2 d = s_dt[t0 + q][my_ch];
-          const State4 Bv = load_state(&s_B[t0 + q][n0]), Cv = load_state(&s_C[t0 + q][n0]);
-          const float2 dt = dup2(d.x), dtu = dup2(d.y);
-          h.lo = __ffma2_rn(ex2_2(__fmul2_rn(dt, A.lo)), h.lo, __fmul2_rn(dtu, Bv.lo));
-          h.hi = __ffma2_rn(ex2_2(__fmul2_rn(dt, A.hi)), h.hi, __fmul2_rn(dtu, Bv.hi));
-          const float2 s = __ffma2_rn(Cv.lo, h.lo, __fmul2_rn(Cv.hi, h.hi));
-          v[q] = s.x + s.y;
-        }
-        LaneSum<L, L / 2, 1>::run(v, lane);
-        s_y[t0 + (lane % L)][my_ch] = v[0];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int t = k * kSsmTile + it + L * i;
-        float r = fmaf(skip, cu[i], s_y[it + L * i][ic]);
-        if (p.z) r *= cz[i] * sigmoid_fast(cz[i]);
-        if (i_on && t < len) {
-          const long long o = b * p.y_b + t * p.y_t + icc;
+    if (role == kStage) {
+      if (first < last) stage_all(true);
+    } else if (role == kWrite) {
+      if (first < last) write_all();
+      if (p.pad_zero && i_on) {
+        const float none[VEC] = {};
+        const int step = TS * (SPLIT ? p.split : 1);
+        for (int t = len + it + TS * rank; t < p.T; t += step) {
+          const long long o = b * p.y_b + (long long)t * p.y_t + icc;
           if (p.out_bf16)
-            static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(r);
+            store_vec<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(p.y) + o, none);
           else
-            static_cast<float*>(p.y)[o] = r;
+            store_vec<float, VEC>(static_cast<float*>(p.y) + o, none);
         }
       }
+    } else {
+      float* chunk = p.h_chunks;
+      if (chunk) chunk += ((size_t)b * ((p.T + kSsmTile - 1) / kSsmTile) + first) * p.D * N + par;
+      for (int k = first; k < last; ++k) {
+        __syncthreads();
+        if (chunk) {
+          if (on) h.store(chunk);
+          chunk += (size_t)p.D * N;
+        }
+        run(k, true);
+      }
+      if (first < last) __syncthreads();
+      if ((!SPLIT || rank + 1 == p.split) && on) h.store(p.h_T + hrow);
     }
-    if ((!SPLIT || rank + 1 == p.split) && on) store_state(p.h_T + hrow, h);
+    if (b + gridDim.y < p.B) __syncthreads();  // the last tile's gates are still being read
   }
 }
 
@@ -321,7 +650,17 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
   const int g = cc / p.per_group;
   const size_t par = (size_t)cc * N + n0;
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    if (p.active && !p.active[b]) continue;
+    const long long o = b * p.y_b + cc;
+    auto put = [&](float r) {
+      if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(r);
+      else
+        static_cast<float*>(p.y)[o] = r;
+    };
+    if (p.active && !p.active[b]) {
+      if (p.pad_zero && on && threadIdx.x % L == 0) put(0.f);
+      continue;
+    }
     float* hp = p.h_T + (size_t)b * p.D * N + par;
     State4 h = load_state(hp), A = load_state(p.A + par);
     float Bv[4], Cv[4];
@@ -350,11 +689,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
     if (threadIdx.x % L == 0) {
       if (p.skip) r = fmaf(p.skip[cc], u, r);
       if (p.z) r *= z * sigmoid_fast(z);
-      const long long o = b * p.y_b + cc;
-      if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(r);
-      else
-        static_cast<float*>(p.y)[o] = r;
+      put(r);
     }
   }
 }

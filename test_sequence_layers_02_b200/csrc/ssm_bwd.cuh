@@ -101,22 +101,22 @@ __global__ void __launch_bounds__(256) ssm_bwd_kernel(const SsmParams p) {
       for (int i = 0; i < IT; ++i) {
         const int t = k * kSsmTile + it + L * i;
         const bool have = i_on && t < len;
-        if (all) ru[i] = have ? up[t * p.u_t] : from_f32<InT>(0.f);
-        rd[i] = have ? dp[t * p.d_t] : from_f32<InT>(0.f);
-        if (p.z) rz[i] = have ? zp[t * p.z_t] : from_f32<InT>(0.f);
+        if (all) ru[i] = have ? up[(long long)t * p.u_t] : from_f32<InT>(0.f);
+        rd[i] = have ? dp[(long long)t * p.d_t] : from_f32<InT>(0.f);
+        if (p.z) rz[i] = have ? zp[(long long)t * p.z_t] : from_f32<InT>(0.f);
         rg[i] = 0.f;
         if (have)
           rg[i] = p.out_bf16
-                      ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dy)[yb + t * p.y_t])
-                      : static_cast<const float*>(p.dy)[yb + t * p.y_t];
+                      ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dy)[yb + (long long)t * p.y_t])
+                      : static_cast<const float*>(p.dy)[yb + (long long)t * p.y_t];
       }
 #pragma unroll
       for (int j = 0; j < S::NBC; ++j) {
         const int e = tid + NT * j;
         const int t = k * kSsmTile + e / N;
         const bool have = e < kSsmTile * N && t < len;
-        if (all) rB[j] = have ? Bp[t * p.Bm_t + e % N] : from_f32<InT>(0.f);
-        rC[j] = have ? Cp[t * p.Cm_t + e % N] : from_f32<InT>(0.f);
+        if (all) rB[j] = have ? Bp[(long long)t * p.Bm_t + e % N] : from_f32<InT>(0.f);
+        rC[j] = have ? Cp[(long long)t * p.Cm_t + e % N] : from_f32<InT>(0.f);
       }
     };
     // behind the length dt = dr = 0: the gradient passes, nothing is added

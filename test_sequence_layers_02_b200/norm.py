@@ -15,8 +15,8 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_device, check_dtype, check_whole, out_dtype_of,
-                       raise_for)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
+                       raise_for, workspace_of, arrays)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 NORM_SUM_BF16 = 1 << 18
@@ -31,56 +31,63 @@ _lib = Library({
 })
 
 
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
 def _rows(name, t, shape, dtype, dev):
-    """The row stride of a tensor of this shape, after its checks."""
-    check(name, t, shape, dtype, dev)
-    if t.dim() == 2:
-        return t.stride(0) if t.shape[0] > 1 else shape[-1]
-    if not t.is_contiguous():
+    """The address and the row stride of a tensor of this shape, after its checks."""
+    p = check(name, t, shape, dtype, dev)
+    if t.is_contiguous():
+        return p, shape[-1]
+    if len(shape) != 2:
         raise ValueError(f"{name}: expected contiguous {tuple(shape)} (2-D tensors may have strides)")
-    return shape[-1]
+    return p, t.stride(0) if shape[0] > 1 else shape[-1]
 
 
 def _strides(D, *lds):
-    return None if all(v == D for v in lds) else (ctypes.c_longlong * 4)(*lds)
+    for v in lds:
+        if v != D:
+            return arrays[4](*lds)
+    return None
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _forward(x, weight, residual, eps, mode, group, y, y_dtype, s, scale_shape, stream):
-    dev, dtype = check_device("x", x), check_dtype("x", x)
-    if x.dim() < 1:
-        raise ValueError("x must be [..., D]")
-    shape = x.shape
+def _shape(name, t):
+    """M, D of a tensor of rows."""
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{name} must be [..., D]")
     D = shape[-1]
-    M = x.numel() // D if D else 0
-    w = check_whole("weight", weight, (D,), torch.float32, dev)
-    ld_x = _rows("x", x, shape, dtype, dev)
-    sum_dtype, ld_r = dtype, D
+    return shape, t.numel() // D if D else 0, D
+
+
+def _forward(x, weight, residual, eps, mode, group, y, y_dtype, s, stream):
+    dev, dtype = cuda_index("x", x), x.dtype
+    shape, M, D = _shape("x", x)
+    w = check_whole("weight", weight, (D,), _F32, dev)
+    xp, ld_x = _rows("x", x, shape, dtype, dev)
+    rp, ld_r, sp, ld_s, sum_dtype = None, D, None, D, dtype
     if residual is not None:
-        sum_dtype = check_dtype("residual", residual)
-        ld_r = _rows("residual", residual, shape, sum_dtype, dev)
+        sum_dtype = residual.dtype
+        cuda_index("residual", residual)
+        rp, ld_r = _rows("residual", residual, shape, sum_dtype, dev)
     elif s is not None:
         raise ValueError("s: there is none without a residual (it would be x)")
-    mode |= ((IN_BF16 if dtype == torch.bfloat16 else 0) |
-             (NORM_SUM_BF16 if sum_dtype == torch.bfloat16 else 0))
+    mode |= ((IN_BF16 if dtype is _BF16 else 0) | (NORM_SUM_BF16 if sum_dtype is _BF16 else 0))
     scale = None
     with On(dev, stream, (x, weight, residual, y, s)) as st:
         if y is None:
             y = torch.empty(shape, dtype=y_dtype, device=dev)
-        ld_y = _rows("y", y, shape, y_dtype, dev)
-        ld_s = D
+        yp, ld_y = _rows("y", y, shape, y_dtype, dev)
         if residual is not None:
             if s is None:
                 s = torch.empty(shape, dtype=sum_dtype, device=dev)
-            ld_s = _rows("s", s, shape, sum_dtype, dev)
-        if scale_shape is not None:
-            scale = torch.empty(shape[:-1] + scale_shape, dtype=torch.float32, device=dev)
-        rc = _lib().ttt_norm_forward(x.data_ptr(), _ptr(residual), w, M, D, eps, mode, group,
-                                     _strides(D, ld_x, ld_r, ld_y, ld_s), y.data_ptr(), _ptr(s),
-                                     _ptr(scale), st)
+            sp, ld_s = _rows("s", s, shape, sum_dtype, dev)
+        if mode & NORM_Y_E4M3:
+            n = -(-D // 128) if group else 1
+            scale = torch.empty(shape[:-1] + (n,), dtype=_F32, device=dev)
+        rc = _lib.ttt_norm_forward(xp, rp, w, M, D, eps, mode, group,
+                                   _strides(D, ld_x, ld_r, ld_y, ld_s), yp, sp,
+                                   None if scale is None else scale.data_ptr(), st)
     raise_for(rc, "ttt_norm_forward")
     return y, scale, x if residual is None else s
 
@@ -95,9 +102,9 @@ def rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, out_dtype: Optional[
     residual's type, or x itself without a residual. ``s`` may be given as the residual (or as x, where the
     types agree) to update the residual stream in place.
     """
-    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, check_dtype("x", x))
-    mode = OUT_BF16 if out_dtype == torch.bfloat16 else 0
-    y, _, s = _forward(x, weight, residual, eps, mode, 0, y, out_dtype, s, None, stream)
+    out_dtype = out_dtype_of(out_dtype, y, x.dtype)
+    mode = OUT_BF16 if out_dtype is _BF16 else 0
+    y, _, s = _forward(x, weight, residual, eps, mode, 0, y, out_dtype, s, stream)
     return y, s
 
 
@@ -111,14 +118,12 @@ def rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
     """
     if group not in (0, 128):
         raise ValueError("group: expected 0 (a scale per row) or 128")
-    n = -(-x.shape[-1] // 128) if group and x.dim() else 1
-    return _forward(x, weight, residual, eps, NORM_Y_E4M3, group, y, torch.float8_e4m3fn, s, (n,),
-                    stream)
+    return _forward(x, weight, residual, eps, NORM_Y_E4M3, group, y, torch.float8_e4m3fn, s, stream)
 
 
 def backward_workspace_bytes(M: int, D: int) -> int:
     """Bytes of device workspace ``ttt_norm_backward`` needs for M rows."""
-    return int(_lib().ttt_norm_backward_workspace_bytes(M, D))
+    return int(_lib.ttt_norm_backward_workspace_bytes(M, D))
 
 
 def rmsnorm_backward(dy, s, weight, ds=None, *, eps: float = 1e-6,
@@ -133,30 +138,22 @@ def rmsnorm_backward(dy, s, weight, ds=None, *, eps: float = 1e-6,
     ``workspace`` (optional): at least ``backward_workspace_bytes`` bytes, not shared by calls that
     overlap.
     """
-    dev, dtype = check_device("s", s), check_dtype("s", s)
-    if s.dim() < 1:
-        raise ValueError("s must be [..., D]")
-    shape = s.shape
-    D = shape[-1]
-    M = s.numel() // D if D else 0
-    w = check_whole("weight", weight, (D,), torch.float32, dev)
-    ld_s = _rows("s", s, shape, dtype, dev)
-    ld_g = _rows("dy", dy, shape, check_dtype("dy", dy), dev)
-    ld_e = D if ds is None else _rows("ds", ds, shape, dtype, dev)
-    mode = ((OUT_BF16 if dy.dtype == torch.bfloat16 else 0) |
-            (NORM_SUM_BF16 if dtype == torch.bfloat16 else 0))
+    dev, dtype = cuda_index("s", s), s.dtype
+    shape, M, D = _shape("s", s)
+    w = check_whole("weight", weight, (D,), _F32, dev)
+    sp, ld_s = _rows("s", s, shape, dtype, dev)
+    check_float("dy", dy, shape, dev)
+    gp, ld_g = _rows("dy", dy, shape, dy.dtype, dev)
+    ep, ld_e = (None, D) if ds is None else _rows("ds", ds, shape, dtype, dev)
+    mode = (OUT_BF16 if dy.dtype is _BF16 else 0) | (NORM_SUM_BF16 if dtype is _BF16 else 0)
     with On(dev, stream, (dy, s, weight, ds, dx, workspace)) as st:
         if dx is None:
             dx = torch.empty(shape, dtype=dtype, device=dev)
-        ld_o = _rows("dx", dx, shape, dtype, dev)
-        need = backward_workspace_bytes(M, D)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        check_whole("workspace", workspace, workspace.shape, workspace.dtype, dev)
+        op, ld_o = _rows("dx", dx, shape, dtype, dev)
+        workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(M, D), dev)
         dweight = torch.empty_like(weight)
-        rc = _lib().ttt_norm_backward(dy.data_ptr(), s.data_ptr(), w, _ptr(ds), M, D, eps, mode,
-                                      _strides(D, ld_g, ld_s, ld_e, ld_o), dx.data_ptr(),
-                                      dweight.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), st)
+        rc = _lib.ttt_norm_backward(gp, sp, w, ep, M, D, eps, mode,
+                                    _strides(D, ld_g, ld_s, ld_e, ld_o), op, dweight.data_ptr(), wp,
+                                    wn, st)
     raise_for(rc, "ttt_norm_backward")
     return dict(dx=dx, dweight=dweight)

@@ -18,11 +18,12 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_device, check_dtype, check_whole, out_dtype_of,
-                       raise_for, strides_of)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
+                       raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 SSM_SOFTPLUS = 1 << 17
+SSM_PAD_ZERO = 1 << 20
 CHUNK = 16  # tokens between two snapshots of the state
 
 _vp, _i, _u, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
@@ -32,36 +33,34 @@ _lib = Library({
     "ttt_ssm_backward": ([_vp] * 9 + [_i] * 5 + [_u] + [_vp] * 14 + [_z, _vp], _i),
     "ttt_ssm_step": ([_vp] * 10 + [_i] * 4 + [_u] + [_vp] * 3, _i),
 })
+_F32, _BF16 = torch.float32, torch.bfloat16
+_ROWS, _TOKENS, _GROUPS = (0,), (0, 1), (0, 1, 2)  # dimensions whose strides count
 
 
-def _mode(in_dtype, out_dtype, softplus) -> int:
-    return ((IN_BF16 if in_dtype == torch.bfloat16 else 0) |
-            (OUT_BF16 if out_dtype == torch.bfloat16 else 0) | (SSM_SOFTPLUS if softplus else 0))
+def _mode(in_dtype, out_dtype, softplus, pad_zero) -> int:
+    return ((IN_BF16 if in_dtype is _BF16 else 0) | (OUT_BF16 if out_dtype is _BF16 else 0) |
+            (SSM_SOFTPLUS if softplus else 0) | (SSM_PAD_ZERO if pad_zero else 0))
 
 
-def _check(u, delta, A, Bm, Cm, D, z, delta_bias):
-    """Shapes and types of what every form takes. Bm and Cm come back with their group dimension."""
-    dev, dtype = check_device("u", u), check_dtype("u", u)
-    if A.dim() != 2:
-        raise ValueError("A must be [D, N]")
-    N = A.shape[1]
-    check("u", u, u.shape, dtype, dev)
-    check("delta", delta, u.shape, dtype, dev)
-    if z is not None:
-        check("z", z, u.shape, dtype, dev)
-    if Bm.dim() == u.dim():
+def _check(u, delta, A, Bm, Cm, D, z, delta_bias, dims):
+    """What every form takes, checked: device, G, N, Bm and Cm with their dimension of groups, and
+    the addresses of u, delta, A, Bm, Cm, D, z, delta_bias."""
+    dev, dtype, shape = cuda_index("u", u), u.dtype, u.shape
+    if len(shape) != dims or A.dim() != 2:
+        raise ValueError("u must be [B, T, D] (a step: [B, D]) and A [D, N]")
+    N, C = A.shape[1], shape[-1]
+    if Bm.dim() == dims:
         Bm, Cm = Bm.unsqueeze(-2), Cm.unsqueeze(-2)
-    if Bm.dim() != u.dim() + 1:
+    if Bm.dim() != dims + 1:
         raise ValueError("Bm must be [B, T, G, N] or [B, T, N] (a step: without T)")
     G = Bm.shape[-2]
-    shape = u.shape[:-1] + (G, N)
-    check("Bm", Bm, shape, dtype, dev)
-    check("Cm", Cm, shape, dtype, dev)
-    ch = (u.shape[-1],)
-    pars = (check_whole("A", A, ch + (N,), torch.float32, dev),
-            check_whole("D", D, ch, torch.float32, dev),
-            check_whole("delta_bias", delta_bias, ch, torch.float32, dev))
-    return dev, dtype, G, N, Bm, Cm, pars
+    bc = shape[:-1] + (G, N)
+    return dev, G, N, Bm, Cm, (
+        check("u", u, shape, dtype, dev), check("delta", delta, shape, dtype, dev),
+        check_whole("A", A, (C, N), _F32, dev), check("Bm", Bm, bc, dtype, dev),
+        check("Cm", Cm, bc, dtype, dev), check_whole("D", D, (C,), _F32, dev),
+        None if z is None else check("z", z, shape, dtype, dev),
+        check_whole("delta_bias", delta_bias, (C,), _F32, dev))
 
 
 def selective_scan(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, *, softplus: bool = True,
@@ -79,39 +78,33 @@ def selective_scan(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, *, soft
     ``want_chunks`` also returns the states before every 16th token, [B, ceil(T/16), D, N], which
     ``selective_scan_backward`` starts from.
     """
-    if u.dim() != 3:
-        raise ValueError("u must be [B, T, D]")
-    dev, dtype, G, N, Bm, Cm, (a, d, bias) = _check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    dev, G, N, Bm, Cm, ptrs = _check(u, delta, A, Bm, Cm, D, z, delta_bias, 3)
     B, T, C = u.shape
-    h = check_whole("h0", h0, (B, C, N), torch.float32, dev)
+    h = check_whole("h0", h0, (B, C, N), _F32, dev)
     n = check_whole("lengths", lengths, (B,), torch.int32, dev)
-    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, dtype)
+    out_dtype = out_dtype_of(out_dtype, y, u.dtype)
+    mode = _mode(u.dtype, out_dtype, softplus, y is None)
     chunks = None
     with On(dev, stream, (u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_T)) as s:
         if y is None:
-            make = torch.empty if lengths is None else torch.zeros
-            y = make(u.shape, dtype=out_dtype, device=dev)
-        else:
-            check("y", y, u.shape, out_dtype, dev)
+            y = torch.empty(u.shape, dtype=out_dtype, device=dev)
+        yp = check("y", y, u.shape, out_dtype, dev)
         if h_T is None:
-            h_T = torch.empty((B, C, N), dtype=torch.float32, device=dev)
-        hT = check_whole("h_T", h_T, (B, C, N), torch.float32, dev)
+            h_T = torch.empty((B, C, N), dtype=_F32, device=dev)
+        hT = check_whole("h_T", h_T, (B, C, N), _F32, dev)
         if want_chunks:
-            chunks = torch.empty((B, -(-T // CHUNK), C, N), dtype=torch.float32, device=dev)
-        st = strides_of((u, (0, 1)), (delta, (0, 1)), (u.shape if z is None else z, (0, 1)),
-                        (Bm, (0, 1, 2)), (Cm, (0, 1, 2)), (y, (0, 1)))
-        rc = _lib().ttt_ssm_forward(
-            u.data_ptr(), delta.data_ptr(), a, Bm.data_ptr(), Cm.data_ptr(), d,
-            None if z is None else z.data_ptr(), bias, h, n, B, T, C, G, N,
-            _mode(dtype, out_dtype, softplus), st, y.data_ptr(), hT,
-            None if chunks is None else chunks.data_ptr(), s)
+            chunks = torch.empty((B, -(-T // CHUNK), C, N), dtype=_F32, device=dev)
+        st = strides_of(14, (u, _TOKENS), (delta, _TOKENS), (u.shape if z is None else z, _TOKENS),
+                        (Bm, _GROUPS), (Cm, _GROUPS), (y, _TOKENS))
+        rc = _lib.ttt_ssm_forward(*ptrs, h, n, B, T, C, G, N, mode, st, yp, hT,
+                                  None if chunks is None else chunks.data_ptr(), s)
     raise_for(rc, "ttt_ssm_forward")
     return (y, h_T, chunks) if want_chunks else (y, h_T)
 
 
 def backward_workspace_bytes(B: int, T: int, D: int, G: int, N: int) -> int:
     """Bytes of device workspace ``ttt_ssm_backward`` needs for these sizes."""
-    return int(_lib().ttt_ssm_backward_workspace_bytes(B, T, D, G, N))
+    return int(_lib.ttt_ssm_backward_workspace_bytes(B, T, D, G, N))
 
 
 def selective_scan_backward(u, delta, A, Bm, Cm, D, z, delta_bias, h_chunks, dy, dh_T=None, *,
@@ -126,37 +119,30 @@ def selective_scan_backward(u, delta, A, Bm, Cm, D, z, delta_bias, h_chunks, dy,
     ``workspace`` (optional): at least ``backward_workspace_bytes`` bytes, not shared by calls that
     overlap.
     """
-    if u.dim() != 3:
-        raise ValueError("u must be [B, T, D]")
     bc_shape = Bm.shape
-    dev, dtype, G, N, Bm, Cm, (a, d, bias) = _check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    dev, G, N, Bm, Cm, ptrs = _check(u, delta, A, Bm, Cm, D, z, delta_bias, 3)
     B, T, C = u.shape
-    check("dy", dy, u.shape, check_dtype("dy", dy), dev)
-    ck = check_whole("h_chunks", h_chunks, (B, -(-T // CHUNK), C, N), torch.float32, dev)
-    dh = check_whole("dh_T", dh_T, (B, C, N), torch.float32, dev)
+    gp = check_float("dy", dy, u.shape, dev)
+    ck = check_whole("h_chunks", h_chunks, (B, -(-T // CHUNK), C, N), _F32, dev)
+    dh = check_whole("dh_T", dh_T, (B, C, N), _F32, dev)
     n = check_whole("lengths", lengths, (B,), torch.int32, dev)
-    st = strides_of((u, (0, 1)), (delta, (0, 1)), (u.shape if z is None else z, (0, 1)),
-                    (Bm, (0, 1, 2)), (Cm, (0, 1, 2)), (dy, (0, 1)))
+    st = strides_of(14, (u, _TOKENS), (delta, _TOKENS), (u.shape if z is None else z, _TOKENS),
+                    (Bm, _GROUPS), (Cm, _GROUPS), (dy, _TOKENS))
     with On(dev, stream, (u, delta, A, Bm, Cm, D, z, delta_bias, h_chunks, dy, dh_T, lengths,
                           workspace)) as s:
-        need = backward_workspace_bytes(B, T, C, G, N)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        check_whole("workspace", workspace, workspace.shape, workspace.dtype, dev)
-        act = dict(dtype=dtype, device=dev)
+        workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(B, T, C, G, N), dev)
+        act = dict(dtype=u.dtype, device=dev)
         out = dict(du=torch.empty(u.shape, **act), ddelta=torch.empty(u.shape, **act),
                    dz=None if z is None else torch.empty(u.shape, **act),
                    dBm=torch.empty(bc_shape, **act), dCm=torch.empty(bc_shape, **act),
                    dA=torch.empty_like(A), dD=None if D is None else torch.empty_like(D),
                    ddelta_bias=None if delta_bias is None else torch.empty_like(delta_bias),
-                   dh0=torch.empty((B, C, N), dtype=torch.float32, device=dev))
+                   dh0=torch.empty((B, C, N), dtype=_F32, device=dev))
         p = {k: None if v is None else v.data_ptr() for k, v in out.items()}
-        rc = _lib().ttt_ssm_backward(
-            u.data_ptr(), delta.data_ptr(), a, Bm.data_ptr(), Cm.data_ptr(), d,
-            None if z is None else z.data_ptr(), bias, n, B, T, C, G, N,
-            _mode(dtype, dy.dtype, softplus), st, ck, dy.data_ptr(), dh, p["du"], p["ddelta"],
-            p["dA"], p["dBm"], p["dCm"], p["dD"], p["dz"], p["ddelta_bias"], p["dh0"],
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+        rc = _lib.ttt_ssm_backward(
+            *ptrs, n, B, T, C, G, N, _mode(u.dtype, dy.dtype, softplus, False), st, ck, gp, dh,
+            p["du"], p["ddelta"], p["dA"], p["dBm"], p["dCm"], p["dD"], p["dz"], p["ddelta_bias"],
+            p["dh0"], wp, wn, s)
     raise_for(rc, "ttt_ssm_backward")
     return out
 
@@ -170,26 +156,20 @@ def selective_step(u, delta, A, Bm, Cm, D, z, delta_bias, h, *, softplus: bool =
     or None, 0 = the row's h and y are left as they were (a y made here is 0 there). D, z and
     delta_bias may be None. A chain of steps equals ``selective_scan``.
     """
-    if u.dim() != 2:
-        raise ValueError("u must be [B, D]")
-    dev, dtype, G, N, Bm, Cm, (a, d, bias) = _check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    dev, G, N, Bm, Cm, ptrs = _check(u, delta, A, Bm, Cm, D, z, delta_bias, 2)
     B, C = u.shape
     if h is None:
         raise ValueError("h: expected the state")
-    hp = check_whole("h", h, (B, C, N), torch.float32, dev)
+    hp = check_whole("h", h, (B, C, N), _F32, dev)
     act = check_whole("active", active, (B,), torch.uint8, dev)
-    out_dtype = out_dtype_of(out_dtype if y is None else y.dtype, dtype)
+    out_dtype = out_dtype_of(out_dtype, y, u.dtype)
+    mode = _mode(u.dtype, out_dtype, softplus, y is None)
     with On(dev, stream, (u, delta, A, Bm, Cm, D, z, delta_bias, h, active, y)) as s:
         if y is None:
-            make = torch.empty if active is None else torch.zeros
-            y = make(u.shape, dtype=out_dtype, device=dev)
-        else:
-            check("y", y, u.shape, out_dtype, dev)
-        st = strides_of((u, (0,)), (delta, (0,)), (u.shape if z is None else z, (0,)),
-                        (Bm, (0, 1)), (Cm, (0, 1)), (y, (0,)))
-        rc = _lib().ttt_ssm_step(
-            u.data_ptr(), delta.data_ptr(), a, Bm.data_ptr(), Cm.data_ptr(), d,
-            None if z is None else z.data_ptr(), bias, hp, act, B, C, G, N,
-            _mode(dtype, out_dtype, softplus), st, y.data_ptr(), s)
+            y = torch.empty(u.shape, dtype=out_dtype, device=dev)
+        yp = check("y", y, u.shape, out_dtype, dev)
+        st = strides_of(8, (u, _ROWS), (delta, _ROWS), (u.shape if z is None else z, _ROWS),
+                        (Bm, _TOKENS), (Cm, _TOKENS), (y, _ROWS))
+        rc = _lib.ttt_ssm_step(*ptrs, hp, act, B, C, G, N, mode, st, yp, s)
     raise_for(rc, "ttt_ssm_step")
     return y

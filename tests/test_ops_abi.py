@@ -23,15 +23,15 @@ def strides(*v):
 @pytest.fixture(scope="module")
 def libs():
     pkg_build.build()
-    from test_sequence_layers_02_b200 import conv, norm, ssm
-    return {"conv": conv._lib(), "ssm": ssm._lib(), "norm": norm._lib()}
+    from test_sequence_layers_02_b200 import conv, norm, ssm  # noqa: F401
+    return {"conv": conv._lib, "ssm": ssm._lib, "norm": norm._lib}
 
 
 CONV = dict(x=addr(0), weight=addr(1), bias=addr(2), state=addr(3), lengths=addr(4), B=2, H=3, T=40, d=8,
             K=4, mode=0, strides=None, y=addr(5), state_T=addr(6))
 BAD_CONV = [dict(x=None), dict(weight=None), dict(y=None), dict(x=addr(0, 2)), dict(weight=addr(1, 4)),
             dict(y=addr(5, 1)), dict(lengths=addr(4, 2)), dict(bias=addr(2, 3)), dict(state=addr(3, 2)),
-            dict(B=-1), dict(H=-1), dict(T=-1), dict(d=0), dict(K=0), dict(mode=1), dict(mode=1 << 20),
+            dict(B=-1), dict(H=-1), dict(T=-1), dict(d=0), dict(K=0), dict(mode=1), dict(mode=1 << 21),
             dict(y=addr(0)), dict(y=addr(0, 400)), dict(y=addr(3)), dict(y=addr(1)), dict(state_T=addr(0)),
             dict(state_T=addr(5, 64)), dict(state_T=addr(3, 4)),
             dict(strides=strides(-960, 320, 8, 960, 320, 8, 72, 24, 8, 72, 24, 8)),
