@@ -30,21 +30,20 @@ int check_sizes(int B, int T, int D, int G, int N, unsigned mode) {
   return TTT_OK;
 }
 
-int channel_tiles(int D, int G, int lanes, int threads) {
-  const int ch = threads / lanes;
-  return (D / G + ch - 1) / ch;
-}
+// Blocks of 32 channels in a group: each has its partial sums of dBm and dCm.
+int channel_blocks(int D, int G) { return (D / G + 31) / 32; }
 
 // CTAs along the tokens for `ctas` pairs of a row and a channel tile. Each CTA of a split runs its
 // span nearly twice, so a split has to bring at least twice the SMs into play: none with
 // more than half an SM's worth of pairs (128 pairs, 4096 tokens, forward: 172 us whole, 248 us
 // in two), then up to two CTAs per SM (32 pairs: 174 us whole, 154 in two, 82 in four, 74 in
-// eight). A span keeps 8 tiles, so that the exchange stays small beside it.
+// eight; backward, 2048 tokens, 291, 201, 111 and 92). A span keeps 4 tiles (777 tokens, 24 pairs,
+// backward: 121 us in four, 76 in eight).
 int split_for(long long ctas, int T, int sms) {
   if (2 * ctas > sms) return 1;
   const int tiles = (T + ttt::kSsmTile - 1) / ttt::kSsmTile;
   int s = 1;
-  while (s < ttt::kSsmMaxSplit && ctas * s <= sms && tiles >= 16 * s) s *= 2;
+  while (s < ttt::kSsmMaxSplit && ctas * s <= sms && tiles >= 8 * s) s *= 2;
   return s;
 }
 
@@ -95,14 +94,24 @@ int launch_fwd(const SsmParams& p, cudaStream_t s) {
   return p.vec ? launch_fwd_as<N, P, InT, 4>(p, s) : launch_fwd_as<N, P, InT, 1>(p, s);
 }
 
-template <int L, typename InT>
-int launch_bwd(const SsmParams& p, cudaStream_t s) {
-  using S = ttt::SsmBwdShape<L>;
-  const long long blocks = (long long)p.tiles * p.G;
+template <int N, int P, typename InT, typename OutT, int VEC>
+int launch_bwd_as(SsmParams p, cudaStream_t s) {
+  using S = ttt::SsmBwdShape<N, P, InT, OutT, VEC>;
+  const long long blocks = (long long)((p.per_group + S::CH - 1) / S::CH) * p.G;
   constexpr size_t smem = sizeof(typename S::Smem);
   return p.split > 1
-             ? launch_kernel(ttt::ssm_bwd_kernel<L, InT, true>, blocks, p.split, p.B, S::NT, smem, p, s)
-             : launch_kernel(ttt::ssm_bwd_kernel<L, InT, false>, blocks, 1, p.B, S::NT, smem, p, s);
+             ? launch_kernel(ttt::ssm_bwd_kernel<N, P, InT, OutT, VEC, true>, blocks, p.split, p.B, S::NT, smem, p, s)
+             : launch_kernel(ttt::ssm_bwd_kernel<N, P, InT, OutT, VEC, false>, blocks, 1, p.B, S::NT, smem, p, s);
+}
+
+template <int L, typename InT>
+int launch_bwd(const SsmParams& p, cudaStream_t s) {
+  constexpr int N = 4 * L;
+  constexpr int P = N <= 16 ? 4 : 8;
+  if (p.out_bf16)
+    return p.vec ? launch_bwd_as<N, P, InT, __nv_bfloat16, 4>(p, s)
+                 : launch_bwd_as<N, P, InT, __nv_bfloat16, 1>(p, s);
+  return p.vec ? launch_bwd_as<N, P, InT, float, 4>(p, s) : launch_bwd_as<N, P, InT, float, 1>(p, s);
 }
 
 template <int L, typename InT>
@@ -181,7 +190,7 @@ bool packs_of_4(const SsmParams& p, std::initializer_list<const void*> in, size_
 
 size_t par_floats(int B, int D, int N) { return (size_t)B * ttt::kSsmMaxSplit * D * (N + 2); }
 size_t bc_floats(int B, int T, int D, int G, int N) {
-  return (size_t)channel_tiles(D, G, N / 4, 256) * B * T * G * 2 * N;
+  return (size_t)channel_blocks(D, G) * B * T * G * 2 * N;
 }
 
 }  // namespace
@@ -291,11 +300,11 @@ int ttt_ssm_backward(const void* u, const void* delta, const float* A, const voi
   p.part_par = p.part_bc + bc_floats(B, T, D, G, N);
   p.B = B; p.T = T; p.D = D; p.G = G;
   p.per_group = D / G;
-  p.tiles = channel_tiles(D, G, N / 4, 256);
+  p.tiles = channel_blocks(D, G);
   p.split = split_for((long long)p.tiles * G * B, T, sm_count());
   p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
   p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
-  p.pad_zero = (mode & TTT_SSM_PAD_ZERO) ? 1 : 0;
+  p.vec = packs_of_4(p, {u, delta, z, Bm, Cm, du, ddelta, dz}, ie, dy, oe) && D % 4 == 0;
   const size_t bc = (size_t)B * T * G * 2 * N;
   const size_t bc_blocks = (bc / 4 + 255) / 256;
   if (bc_blocks > 0x7fffffffULL || (long long)B * p.split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;

@@ -14,6 +14,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "seq_common.cuh"
 
 namespace ttt {

@@ -11,74 +11,109 @@
 //     dA += g q dt                           (summed over rows and tokens)
 //     g  <- a_t g
 //
-// The states come from the forward's snapshots, 16 tokens apart: a tile is walked
-// in two halves of 8 tokens, whose decays and q stay in registers between the
-// way forward and the way back (the later half first, after a run over the earlier
-// half for its end state: half a tile's exponentials more, where snapshots every 8
-// tokens would be as much traffic as u, delta, z and dy together).
+// The states come from the forward's snapshots, 16 tokens apart. A tile is walked in four
+// quarters of 4 tokens, the last first: a run over its first 12 tokens leaves the states before
+// the quarters, and each quarter's decays and q stay in registers between its way forward
+// and its way back. That is 1.75 exponentials a token; with halves of 8 tokens it would be 1.5,
+// but the registers of a half leave an SM one CTA in place of two.
 //
-// Work: about 20 fp32 operations, 1.5 exponentials and two lane sums per state of
-// every (token, channel); the fp32 and shuffle issue binds, not HBM.
+// Work: about 25 packed fp32 operations and 1.75 exponentials for 4 states of a (token,
+// channel), and two sums over the channels for each (token, state): at N = 16, 32 values a lane
+// (four tokens) over a warp's 32 channels in five scatter steps, 31 shuffles where adding
+// value by value would be 160 (and where four times the steps for one token each took a fifth
+// longer: the steps wait for one another). The issue of all that binds, not HBM and not the special-function units.
+// The sums over channel tiles go through partial sums in global memory, added in tile
+// order. No atomics: the same bits on every call.
 //
-// The sums over the channels of dBm and dCm: 8 values a lane are added over a warp's
-// channels by scatter steps (7 shuffles for 8 values), over the CTA's warps
-// in shared memory, and over the channel tiles from partial sums in global memory
-// in tile order. No atomics: the same bits on every call.
+// Measured, bf16, N = 16, with the reductions: 8 x 4096 tokens by 768 channels 0.90 ms, 16 x 2048 by 1536
+// 1.35 ms, 4 x 2048 by 256 0.09 ms; about 0.47 instructions a clock and scheduler.
 #pragma once
 
 #include "ssm.cuh"
 
 namespace ttt {
 
-template <int L>
+// Roles as in the forward, with one set of four warps around the recurrence: between two
+// barriers the recurrence takes tile k (from the last down), the others finish tile k + 1
+// and stage tile k - 1. A tile's sums (s1 .. s3, dBm, dCm) have one buffer: the others
+// read it at once, and the recurrence waits for that at a second barrier, behind its
+// run over the first 12 tokens.
+template <int N, int P, typename InT, typename OutT, int VEC>
 struct SsmBwdShape {
-  static constexpr int NT = 256;
-  static constexpr int N = 4 * L;
-  static constexpr int CH = NT / L;
-  static constexpr int IT = kSsmTile / L;
-  static constexpr int NBC = (kSsmTile * N + NT - 1) / NT;
-  static constexpr int ROW = CH + 32 / L;       // row of the s1, s2, s3 tiles
-  static constexpr int V = L < 4 ? L : 4;       // tokens whose s-sums are added at once
-  static constexpr int kHalf = 8;
+  static constexpr int L = N / P;               // warps that share a channel
+  static constexpr int CW = L < 4 ? 4 / L : 1;  // blocks of 32 channels
+  static constexpr int CH = 32 * CW;
+  static constexpr int RT = CH * L;             // threads of the recurrence
+  static constexpr int HT = 128;                // threads around it
+  static constexpr int NT = RT + HT;
+  static constexpr int QUADS = CH / VEC;
+  static constexpr int TS = HT / QUADS;         // tokens between a thread's items
+  static constexpr int IT = kSsmTile / TS;      // items per thread and tile
+  static constexpr int BCQ = kSsmTile * N / VEC;
+  static constexpr int NBC = (BCQ + HT - 1) / HT;
+  // Slots of raw inputs: from the copy to the end of the tile's epilogue, two tiles after
+  // its use in staging.
+  static constexpr int RING = VEC == 1 ? 4 : sizeof(InT) == 2 ? 6 : 5;
+  static constexpr int AHEAD = RING - 3;        // tiles on their way
+  static constexpr int SUMS = CW * kSsmTile * 2 * N;
   struct Smem {
-    float2 dt[kSsmTile][CH];                    // dt, dt u
-    float dr[kSsmTile][CH];
-    alignas(16) float B[kSsmTile][N];
-    alignas(16) float C[kSsmTile][N];
-    float s1[kSsmTile][ROW], s2[kSsmTile][ROW], s3[kSsmTile][ROW];
-    alignas(16) float part[NT / 32][kSsmTile][2 * N];
-    float4 start[NT], decay[NT];                // exchange of a cluster
+    alignas(16) float2 dt[2][kSsmTile][CH];     // dt, dt u
+    alignas(16) float dr[2][kSsmTile][CH];
+    alignas(16) float B[2][kSsmTile][N];
+    alignas(16) float C[2][kSsmTile][N];
+    alignas(16) float s[3][kSsmTile][L][CH];    // s1, s2, s3: a part for each of a channel's warps
+    alignas(16) float bc[CW][kSsmTile][2 * N];  // dBm, dCm of 32 channels
+    struct Slot {
+      Pack<InT, VEC> u[IT][HT], d[IT][HT], z[IT][HT], B[NBC][HT], C[NBC][HT];
+      Pack<OutT, VEC> g[IT][HT];
+    } ring[RING];
   };
 };
 
-template <int L, typename InT, bool SPLIT>
-__global__ void __launch_bounds__(256) ssm_bwd_kernel(const SsmParams p) {
-  using S = SsmBwdShape<L>;
-  constexpr int N = S::N, CH = S::CH, IT = S::IT, NT = S::NT, V = S::V, kHalf = S::kHalf;
+template <int N, int P, typename InT, typename OutT, int VEC, bool SPLIT>
+__global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16 ? 2 : 1)
+    ssm_bwd_kernel(const SsmParams p) {
+  using S = SsmBwdShape<N, P, InT, OutT, VEC>;
+  constexpr int L = S::L, CW = S::CW, CH = S::CH, IT = S::IT, TS = S::TS, RT = S::RT, HT = S::HT;
+  constexpr int NBC = S::NBC, QUADS = S::QUADS, RING = S::RING, AHEAD = S::AHEAD;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(smem_raw);
+  __shared__ float2 s_start[SPLIT ? P / 2 : 1][SPLIT ? RT : 1], s_decay[SPLIT ? P / 2 : 1][SPLIT ? RT : 1];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool recur = threadIdx.x < RT;
+  const int tid = recur ? threadIdx.x : threadIdx.x - RT;  // within the role
+  const int lane = threadIdx.x & 31;
   const int rank = SPLIT ? blockIdx.x % p.split : 0;
   const int tile = SPLIT ? blockIdx.x / p.split : blockIdx.x;
-  const int g = tile / p.tiles;
-  const int tile_in_group = tile - g * p.tiles;
+  const int cta_tiles = (p.per_group + CH - 1) / CH;
+  const int g = tile / cta_tiles;
+  const int tile_in_group = tile - g * cta_tiles;
   const int in_group = tile_in_group * CH;
   const int c0 = g * p.per_group + in_group;
   const int nch = min(CH, p.per_group - in_group);
 
-  const int my_ch = warp * (32 / L) + lane / L;
-  const int n0 = (lane % L) * 4;
-  const bool on = my_ch < nch;
+  // the recurrence: states n0 .. n0 + P - 1 of channel my_ch
+  const int part = (tid >> 5) % L;
+  const int block = (tid >> 5) / L;
+  const int my_ch = (block * 32 + lane) % CH;
+  const int n0 = part * P;
+  const bool on = recur && my_ch < nch;
   const size_t par = (size_t)(c0 + (on ? my_ch : 0)) * N + n0;
-  State4 A = load_state(p.A + par);
-  A.lo.x *= kLog2e; A.lo.y *= kLog2e; A.hi.x *= kLog2e; A.hi.y *= kLog2e;
+  States<P> A;
+  A.load(p.A + par);
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) A.v[i] = __fmul2_rn(A.v[i], dup2(kLog2e));
 
-  const int ic = tid % CH, it = tid / CH;
+  // the others: tokens it + TS i of channels ic .. ic + VEC - 1
+  const int ic = tid % QUADS * VEC, it = tid / QUADS;
   const bool i_on = ic < nch;
   const int icc = c0 + (i_on ? ic : 0);
-  const float bias = p.delta_bias ? p.delta_bias[icc] : 0.f;
-  const float skip = p.skip ? p.skip[icc] : 0.f;
+  float bias[VEC], skip[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) {
+    bias[q] = p.delta_bias ? p.delta_bias[icc + q] : 0.f;
+    skip[q] = p.skip ? p.skip[icc + q] : 0.f;
+  }
 
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int len = ssm_length(p.lengths, b, p.T);
@@ -86,267 +121,409 @@ __global__ void __launch_bounds__(256) ssm_bwd_kernel(const SsmParams p) {
     const int per = SPLIT ? (n_tiles + p.split - 1) / p.split : n_tiles;
     const int first = min(n_tiles, rank * per), last = min(n_tiles, first + per);
 
-    const InT* up = static_cast<const InT*>(p.u) + b * p.u_b + icc;
-    const InT* dp = static_cast<const InT*>(p.delta) + b * p.d_b + icc;
-    const InT* zp = static_cast<const InT*>(p.z) + b * p.z_b + icc;
-    const InT* Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g;
-    const InT* Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g;
-    const long long yb = b * p.y_b + icc;
-    const size_t ob = (size_t)b * p.T * p.D + icc;  // du, ddelta, dz
-
-    InT ru[IT], rd[IT], rz[IT], rB[S::NBC], rC[S::NBC];
-    float rg[IT];
-    auto fetch = [&](int k, bool all) {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int t = k * kSsmTile + it + L * i;
-        const bool have = i_on && t < len;
-        if (all) ru[i] = have ? up[(long long)t * p.u_t] : from_f32<InT>(0.f);
-        rd[i] = have ? dp[(long long)t * p.d_t] : from_f32<InT>(0.f);
-        if (p.z) rz[i] = have ? zp[(long long)t * p.z_t] : from_f32<InT>(0.f);
-        rg[i] = 0.f;
-        if (have)
-          rg[i] = p.out_bf16
-                      ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dy)[yb + (long long)t * p.y_t])
-                      : static_cast<const float*>(p.dy)[yb + (long long)t * p.y_t];
-      }
-#pragma unroll
-      for (int j = 0; j < S::NBC; ++j) {
-        const int e = tid + NT * j;
-        const int t = k * kSsmTile + e / N;
-        const bool have = e < kSsmTile * N && t < len;
-        if (all) rB[j] = have ? Bp[(long long)t * p.Bm_t + e % N] : from_f32<InT>(0.f);
-        rC[j] = have ? Cp[(long long)t * p.Cm_t + e % N] : from_f32<InT>(0.f);
-      }
+    // ---- around the recurrence ----
+    const InT *up, *dp, *zp, *Bp, *Cp;
+    const OutT* gp;
+    const bool bc_on = S::BCQ % HT == 0 || tid < S::BCQ;
+    constexpr int BROW = N / VEC, BS = HT / BROW;
+    const int bt = tid / BROW, bn = tid % BROW * VEC;
+    // Pointers to a thread's items and packs of tile k, which move down a tile at a time.
+    auto seek = [&](int k) {
+      const long long t0 = (long long)k * kSsmTile + it, e0 = (long long)k * kSsmTile + bt;
+      up = static_cast<const InT*>(p.u) + b * p.u_b + t0 * p.u_t + icc;
+      dp = static_cast<const InT*>(p.delta) + b * p.d_b + t0 * p.d_t + icc;
+      zp = static_cast<const InT*>(p.z) + b * p.z_b + t0 * p.z_t + icc;
+      gp = static_cast<const OutT*>(p.dy) + b * p.y_b + t0 * p.y_t + icc;
+      Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g + e0 * p.Bm_t + bn;
+      Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g + e0 * p.Cm_t + bn;
     };
-    // behind the length dt = dr = 0: the gradient passes, nothing is added
-    auto stage = [&](int k, bool all) {
+    auto slot = [&](int k) -> typename S::Smem::Slot& { return sm.ring[k % RING]; };
+    // The inputs of tile k on their way to its slot (0 behind the length); one group of
+    // copies a tile, also an empty one below the first. Single elements go through a register.
+    auto send = [&](int k) {
+      if (k >= first) {
+        typename S::Smem::Slot& r = slot(k);
+        const int left = len - k * kSsmTile;
+        auto move = [&](auto& dst, const auto* src, bool have) {
+          using T = std::remove_reference_t<decltype(dst)>;
+          if constexpr (VEC > 1) {
+            copy_async<sizeof(T)>(&dst, src, have);
+          } else {
+            T x = {};
+            if (have) x = *reinterpret_cast<const T*>(src);
+            dst = x;
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const bool have = it + TS * i < left;
+          move(r.u[i][tid], have ? up + TS * i * p.u_t : up, have);
+          move(r.d[i][tid], have ? dp + TS * i * p.d_t : dp, have);
+          if (p.z) move(r.z[i][tid], have ? zp + TS * i * p.z_t : zp, have);
+          move(r.g[i][tid], have ? gp + TS * i * p.y_t : gp, have);
+        }
+        if (bc_on) {
+#pragma unroll
+          for (int j = 0; j < NBC; ++j) {
+            const bool have = bt + BS * j < left;
+            move(r.B[j][tid], have ? Bp + BS * j * p.Bm_t : Bp, have);
+            move(r.C[j][tid], have ? Cp + BS * j * p.Cm_t : Cp, have);
+          }
+        }
+        up -= kSsmTile * p.u_t;
+        dp -= kSsmTile * p.d_t;
+        zp -= kSsmTile * p.z_t;
+        gp -= kSsmTile * p.y_t;
+        Bp -= kSsmTile * p.Bm_t;
+        Cp -= kSsmTile * p.Cm_t;
+      }
+      if constexpr (VEC > 1) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Tile k from its slot to the recurrence's half of shared memory. Behind the length, and
+    // in channels that are not there, dt = dr = 0: the gradient passes, nothing is added.
+    auto stage = [&](int k) {
+      if constexpr (VEC > 1) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+      const typename S::Smem::Slot& f = slot(k);
+      const int h = k & 1, left = i_on ? len - k * kSsmTile : 0;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int t = it + L * i;
-        const float x = to_f32(rd[i]) + bias;
-        float dt = p.softplus ? softplus(x) : x;
-        if (k * kSsmTile + t >= len || !i_on) dt = 0.f;
-        float dr = rg[i];
+        const int t = it + TS * i;
+        float dt[VEC], u[VEC], dr[VEC];
+        f.d[i][tid].widen(dt);
+        f.u[i][tid].widen(u);
+        f.g[i][tid].widen(dr);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) dt[q] += bias[q];
+        if (p.softplus) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) dt[q] = softplus(dt[q]);
+        }
         if (p.z) {
-          const float z = to_f32(rz[i]);
-          dr *= z * sigmoid_fast(z);
-        }
-        sm.dt[t][ic] = make_float2(dt, all ? dt * to_f32(ru[i]) : 0.f);
-        sm.dr[t][ic] = dr;
-      }
+          float z[VEC];
+          f.z[i][tid].widen(z);
 #pragma unroll
-      for (int j = 0; j < S::NBC; ++j) {
-        const int e = tid + NT * j;
-        if (e < kSsmTile * N) {
-          if (all) (&sm.B[0][0])[e] = to_f32(rB[j]);
-          (&sm.C[0][0])[e] = to_f32(rC[j]);
+          for (int q = 0; q < VEC; ++q) dr[q] *= z[q] * sigmoid_fast(z[q]);
+        }
+        if (t >= left) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) dt[q] = dr[q] = 0.f;
+        }
+        if constexpr (VEC == 1) {
+          sm.dt[h][t][ic] = make_float2(dt[0], dt[0] * u[0]);
+        } else {
+          float4* o = reinterpret_cast<float4*>(&sm.dt[h][t][ic]);
+#pragma unroll
+          for (int q = 0; q < VEC; q += 2)
+            o[q / 2] = make_float4(dt[q], dt[q] * u[q], dt[q + 1], dt[q + 1] * u[q + 1]);
+        }
+        store_vec<float, VEC>(&sm.dr[h][t][ic], dr);
+      }
+      if (bc_on) {
+#pragma unroll
+        for (int j = 0; j < NBC; ++j) {
+          float v[VEC];
+          f.B[j][tid].widen(v);
+          store_vec<float, VEC>(&sm.B[h][bt + BS * j][bn], v);
+          f.C[j][tid].widen(v);
+          store_vec<float, VEC>(&sm.C[h][bt + BS * j][bn], v);
         }
       }
     };
 
+    float dskip[VEC], dbias[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) dskip[q] = dbias[q] = 0.f;
+    const size_t ob = (size_t)b * p.T * p.D + icc;  // du, ddelta, dz
+    // Tile k behind the recurrence: first the sums out of their buffers (then `free`), then the
+    // gradients of u, delta and z and the partial sums of dBm and dCm.
+    auto finish = [&](int k, auto free) {
+      const int h = k & 1;
+      const typename S::Smem::Slot& f = slot(k);
+      float s1[IT][VEC], s2[IT][VEC], s3[IT][VEC];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int t = it + TS * i;
+        load_vec<float, VEC>(&sm.s[0][t][0][ic], s1[i]);
+        load_vec<float, VEC>(&sm.s[1][t][0][ic], s2[i]);
+        load_vec<float, VEC>(&sm.s[2][t][0][ic], s3[i]);
+#pragma unroll
+        for (int j = 1; j < L; ++j) {
+          float v[3][VEC];
+          load_vec<float, VEC>(&sm.s[0][t][j][ic], v[0]);
+          load_vec<float, VEC>(&sm.s[1][t][j][ic], v[1]);
+          load_vec<float, VEC>(&sm.s[2][t][j][ic], v[2]);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) {
+            s1[i][q] += v[0][q];
+            s2[i][q] += v[1][q];
+            s3[i][q] += v[2][q];
+          }
+        }
+      }
+      const int left_all = len - k * kSsmTile;
+#pragma unroll
+      for (int e = tid * 4; e < S::SUMS; e += HT * 4) {
+        const int cw = e / (kSsmTile * 2 * N), t = e / (2 * N) % kSsmTile, n = e % (2 * N);
+        if (t < left_all && cw * 32 < nch) {
+          const size_t row =
+              (((size_t)(tile_in_group * CW + cw) * p.B + b) * p.T + (size_t)k * kSsmTile + t) * p.G + g;
+          *reinterpret_cast<float4*>(p.part_bc + row * (2 * N) + n) =
+              *reinterpret_cast<const float4*>(&sm.bc[0][0][0] + e);
+        }
+      }
+      free();
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int tt = it + TS * i, t = k * kSsmTile + tt;
+        if (!i_on || t >= p.T) continue;
+        float du[VEC], dd[VEC], dz[VEC], u[VEC], x[VEC], dr[VEC];
+        f.u[i][tid].widen(u);
+        f.d[i][tid].widen(x);
+        load_vec<float, VEC>(&sm.dr[h][tt][ic], dr);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          du[q] = fmaf(sm.dt[h][tt][ic + q].x, s1[i][q], skip[q] * dr[q]);
+          dd[q] = fmaf(u[q], s1[i][q], s2[i][q] * (1.0f / kLog2e));  // A was scaled by log2 e
+          if (p.softplus) dd[q] *= sigmoid_fast(x[q] + bias[q]);
+        }
+        if (p.z) {
+          float z[VEC], dy[VEC];
+          f.z[i][tid].widen(z);
+          f.g[i][tid].widen(dy);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) {
+            const float sg = sigmoid_fast(z[q]);
+            dz[q] = dy[q] * fmaf(skip[q], u[q], s3[i][q]) * sg * fmaf(z[q], 1.f - sg, 1.f);
+          }
+        }
+        if (t >= len) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) du[q] = dd[q] = dz[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          dskip[q] = fmaf(dr[q], u[q], dskip[q]);
+          dbias[q] += dd[q];
+        }
+        const size_t o = ob + (size_t)t * p.D;
+        store_vec<InT, VEC>(static_cast<InT*>(p.du) + o, du);
+        store_vec<InT, VEC>(static_cast<InT*>(p.ddelta) + o, dd);
+        if (p.z) store_vec<InT, VEC>(static_cast<InT*>(p.dz) + o, dz);
+      }
+    };
+
+    // ---- the recurrence ----
     const size_t hrow = (size_t)b * p.D * N + par;
-    State4 gr = {dup2(0.f), dup2(0.f)};  // gradient of the state after the tokens still to come
+    States<P> gr;  // gradient of the state after the tokens still to come
+    gr.zero();
+    // one token on the way forward
+    auto ahead = [&](int half, int t, States<P>& h, States<P>& at, States<P>& qt) {
+      const float2 d = sm.dt[half][t][my_ch];
+      States<P> Bv;
+      Bv.load(&sm.B[half][t][n0]);
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) {
+        at.v[i] = ex2_2(__fmul2_rn(dup2(d.x), A.v[i]));
+        qt.v[i] = __fmul2_rn(at.v[i], h.v[i]);
+        h.v[i] = __ffma2_rn(dup2(d.y), Bv.v[i], qt.v[i]);
+      }
+    };
 
     if constexpr (SPLIT) {
       namespace cg = cooperative_groups;
       cg::cluster_group cluster = cg::this_cluster();
       float sum_dt = 0.f;
-      if (rank > 0) {
-        if (first < last) fetch(last - 1, false);
-        for (int k = last - 1; k >= first; --k) {
-          stage(k, false);
-          __syncthreads();
-          if (k > first) fetch(k - 1, false);
-#pragma unroll
-          for (int t = kSsmTile - 1; t >= 0; --t) {
-            const float2 dt = dup2(sm.dt[t][my_ch].x), dr = dup2(sm.dr[t][my_ch]);
-            const State4 Cv = load_state(&sm.C[t][n0]);
-            gr.lo = __fmul2_rn(ex2_2(__fmul2_rn(dt, A.lo)), __ffma2_rn(Cv.lo, dr, gr.lo));
-            gr.hi = __fmul2_rn(ex2_2(__fmul2_rn(dt, A.hi)), __ffma2_rn(Cv.hi, dr, gr.hi));
-            sum_dt += dt.x;
-          }
-          __syncthreads();
+      if (rank > 0 && first < last) {
+        if (!recur) {
+          seek(last - 1);
+          for (int j = 0; j < AHEAD; ++j) send(last - 1 - j);
+          stage(last - 1);
+          send(last - 1 - AHEAD);
         }
+        for (int k = last - 1; k >= first; --k) {
+          __syncthreads();
+          if (recur) {
+#pragma unroll
+            for (int t = kSsmTile - 1; t >= 0; --t) {
+              const float2 dt = dup2(sm.dt[k & 1][t][my_ch].x), dr = dup2(sm.dr[k & 1][t][my_ch]);
+              States<P> Cv;
+              Cv.load(&sm.C[k & 1][t][n0]);
+#pragma unroll
+              for (int i = 0; i < P / 2; ++i)
+                gr.v[i] = __fmul2_rn(ex2_2(__fmul2_rn(dt, A.v[i])), __ffma2_rn(Cv.v[i], dr, gr.v[i]));
+              sum_dt += dt.x;
+            }
+          } else if (k > first) {
+            stage(k - 1);
+            send(k - 1 - AHEAD);
+          }
+        }
+        if constexpr (VEC > 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      const float2 lo = ex2_2(__fmul2_rn(dup2(sum_dt), A.lo));
-      const float2 hi = ex2_2(__fmul2_rn(dup2(sum_dt), A.hi));
-      sm.start[tid] = make_float4(gr.lo.x, gr.lo.y, gr.hi.x, gr.hi.y);
-      sm.decay[tid] = make_float4(lo.x, lo.y, hi.x, hi.y);
-      gr = p.dh_T ? load_state(p.dh_T + hrow) : State4{dup2(0.f), dup2(0.f)};
+      if (recur) {
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          s_start[i][tid] = gr.v[i];
+          s_decay[i][tid] = ex2_2(__fmul2_rn(dup2(sum_dt), A.v[i]));
+        }
+        gr.zero();
+        if (p.dh_T) gr.load(p.dh_T + hrow);
+      }
       cluster.sync();
-      for (int r = p.split - 1; r > rank; --r) {
-        const float4 e = *cluster.map_shared_rank(&sm.start[tid], r);
-        const float4 a = *cluster.map_shared_rank(&sm.decay[tid], r);
-        gr.lo = __ffma2_rn(make_float2(a.x, a.y), gr.lo, make_float2(e.x, e.y));
-        gr.hi = __ffma2_rn(make_float2(a.z, a.w), gr.hi, make_float2(e.z, e.w));
+      if (recur) {
+        for (int r = p.split - 1; r > rank; --r) {
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i)
+            gr.v[i] = __ffma2_rn(*cluster.map_shared_rank(&s_decay[i][tid], r), gr.v[i],
+                                 *cluster.map_shared_rank(&s_start[i][tid], r));
+        }
       }
       cluster.sync();  // nobody writes or leaves while its shared memory is read
     } else {
-      if (p.dh_T) gr = load_state(p.dh_T + hrow);
+      if (recur && p.dh_T) gr.load(p.dh_T + hrow);
     }
 
-    State4 dA = {dup2(0.f), dup2(0.f)};
-    float dskip = 0.f, dbias = 0.f;
-    const float* chunks =
-        p.h_chunks + (size_t)b * ((p.T + kSsmTile - 1) / kSsmTile) * p.D * N + par;
-    State4 snap_next = {dup2(0.f), dup2(0.f)};
-    if (first < last) {
-      fetch(last - 1, true);
-      snap_next = load_state(chunks + (size_t)(last - 1) * p.D * N);
-    }
-    for (int k = last - 1; k >= first; --k) {
-      stage(k, true);
-      float cu[IT], cx[IT], cz[IT], cg_[IT];
+    // The second barrier of a tile: its sums of the tile before have been read.
+    auto sums_read = [] { asm volatile("bar.arrive 1, %0;" ::"n"(S::NT) : "memory"); };
+    if (recur) {
+      States<P> dA;
+      dA.zero();
+      const float* chunks =
+          p.h_chunks + (size_t)b * ((p.T + kSsmTile - 1) / kSsmTile) * p.D * N + par;
+      States<P> next;
+      next.zero();
+      if (first < last) next.load(chunks + (size_t)(last - 1) * p.D * N);
+      for (int k = last - 1; k >= first; --k) {
+        const int half = k & 1;
+        __syncthreads();
+        States<P> before[4];  // the state before each quarter
+        before[0] = next;
+        if (k > first) next.load(chunks + (size_t)(k - 1) * p.D * N);
+        {
+          States<P> h = before[0], x, y;
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        cu[i] = to_f32(ru[i]);
-        cx[i] = to_f32(rd[i]) + bias;
-        cz[i] = p.z ? to_f32(rz[i]) : 0.f;
-        cg_[i] = rg[i];
-      }
-      const State4 snap = snap_next;
-      __syncthreads();
-      if (k > first) {
-        fetch(k - 1, true);
-        snap_next = load_state(chunks + (size_t)(k - 1) * p.D * N);
-      }
-
-      State4 a[kHalf], q[kHalf];
-      // one token on the way forward
-      auto ahead = [&](int t, State4& h, State4& at, State4& qt) {
-        const float2 d = sm.dt[t][my_ch];
-        const State4 Bv = load_state(&sm.B[t][n0]);
-        const float2 dt = dup2(d.x), dtu = dup2(d.y);
-        at.lo = ex2_2(__fmul2_rn(dt, A.lo));
-        at.hi = ex2_2(__fmul2_rn(dt, A.hi));
-        qt.lo = __fmul2_rn(at.lo, h.lo);
-        qt.hi = __fmul2_rn(at.hi, h.hi);
-        h.lo = __ffma2_rn(dtu, Bv.lo, qt.lo);
-        h.hi = __ffma2_rn(dtu, Bv.hi, qt.hi);
-      };
-#pragma unroll 1
-      for (int half = 1; half >= 0; --half) {
-        State4 h = snap;
-        if (half) {
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) {
-            State4 x, y;
-            ahead(j, h, x, y);
+          for (int t = 0; t < 12; ++t) {
+            ahead(half, t, h, x, y);
+            if (t % 4 == 3) before[t / 4 + 1] = h;
           }
         }
-        const int base = half * kHalf;
+        asm volatile("bar.sync 1, %0;" ::"n"(S::NT) : "memory");
+#pragma unroll 1
+        for (int quarter = 3; quarter >= 0; --quarter) {
+          States<P> a[4], q[4], h = before[3];
+          before[3] = before[2];
+          before[2] = before[1];
+          before[1] = before[0];
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) ahead(base + j, h, a[j], q[j]);
-        float v1[V], v2[V], v3[V];
+          for (int j = 0; j < 4; ++j) ahead(half, quarter * 4 + j, h, a[j], q[j]);
+          constexpr int SET = P == 4 ? 4 : 2;  // tokens whose sums are taken at once
+          float w[SET * 2 * P];
 #pragma unroll
-        for (int j = kHalf - 1; j >= 0; --j) {
-          const int t = base + j;
-          const float2 d = sm.dt[t][my_ch];
-          const float2 dt = dup2(d.x), dtu = dup2(d.y), dr = dup2(sm.dr[t][my_ch]);
-          const State4 Bv = load_state(&sm.B[t][n0]), Cv = load_state(&sm.C[t][n0]);
-          gr.lo = __ffma2_rn(Cv.lo, dr, gr.lo);
-          gr.hi = __ffma2_rn(Cv.hi, dr, gr.hi);
-          const float2 hlo = __ffma2_rn(dtu, Bv.lo, q[j].lo), hhi = __ffma2_rn(dtu, Bv.hi, q[j].hi);
-          const float2 clo = __fmul2_rn(dr, hlo), chi = __fmul2_rn(dr, hhi);
-          const float2 blo = __fmul2_rn(gr.lo, dtu), bhi = __fmul2_rn(gr.hi, dtu);
-          const float2 x1 = __ffma2_rn(gr.lo, Bv.lo, __fmul2_rn(gr.hi, Bv.hi));
-          const float2 x3 = __ffma2_rn(Cv.lo, hlo, __fmul2_rn(Cv.hi, hhi));
-          const float2 qlo = __fmul2_rn(gr.lo, q[j].lo), qhi = __fmul2_rn(gr.hi, q[j].hi);
-          const float2 x2 = __ffma2_rn(qlo, A.lo, __fmul2_rn(qhi, A.hi));
-          dA.lo = __ffma2_rn(qlo, dt, dA.lo);
-          dA.hi = __ffma2_rn(qhi, dt, dA.hi);
-          gr.lo = __fmul2_rn(a[j].lo, gr.lo);
-          gr.hi = __fmul2_rn(a[j].hi, gr.hi);
-          v1[j % V] = x1.x + x1.y;
-          v2[j % V] = x2.x + x2.y;
-          v3[j % V] = x3.x + x3.y;
-          // dBm, dCm of this token, over the warp's channels
-          using Over = LaneSum<8, 16, L>;
-          float w[8] = {blo.x, blo.y, bhi.x, bhi.y, clo.x, clo.y, chi.x, chi.y};
-          Over::run(w, lane);
-          if ((lane & Over::copies) == 0) {
-            const int f = Over::first(lane);
-            float* dst = &sm.part[warp][t][(f < 4 ? n0 : N + n0 - 4) + f];
+          for (int j = 3; j >= 0; --j) {
+            float* wj = w + j % SET * 2 * P;
+            const int t = quarter * 4 + j;
+            const float2 d = sm.dt[half][t][my_ch];
+            const float2 dt = dup2(d.x), dtu = dup2(d.y), dr = dup2(sm.dr[half][t][my_ch]);
+            States<P> Bv, Cv;
+            Bv.load(&sm.B[half][t][n0]);
+            Cv.load(&sm.C[half][t][n0]);
+            float2 x1, x2, x3;
 #pragma unroll
-            for (int m = 0; m < Over::left; ++m) dst[m] = w[m];
-          }
-          if (j % V == 0) {
-            // s1, s2, s3 of V tokens, over a channel's lanes
-            using Sum = LaneSum<V, L / 2, 1>;
-            Sum::run(v1, lane);
-            Sum::run(v2, lane);
-            Sum::run(v3, lane);
-            if ((lane & Sum::copies) == 0) {
-              const int tt = t + Sum::first(lane);
-              sm.s1[tt][my_ch] = v1[0];
-              sm.s2[tt][my_ch] = v2[0];
-              sm.s3[tt][my_ch] = v3[0];
+            for (int i = 0; i < P / 2; ++i) {
+              gr.v[i] = __ffma2_rn(Cv.v[i], dr, gr.v[i]);
+              const float2 hh = __ffma2_rn(dtu, Bv.v[i], q[j].v[i]);
+              const float2 cc = __fmul2_rn(dr, hh), bb = __fmul2_rn(gr.v[i], dtu);
+              wj[2 * i] = bb.x;
+              wj[2 * i + 1] = bb.y;
+              wj[P + 2 * i] = cc.x;
+              wj[P + 2 * i + 1] = cc.y;
+              const float2 gq = __fmul2_rn(gr.v[i], q[j].v[i]);
+              x1 = i ? __ffma2_rn(gr.v[i], Bv.v[i], x1) : __fmul2_rn(gr.v[i], Bv.v[i]);
+              x2 = i ? __ffma2_rn(gq, A.v[i], x2) : __fmul2_rn(gq, A.v[i]);
+              x3 = i ? __ffma2_rn(Cv.v[i], hh, x3) : __fmul2_rn(Cv.v[i], hh);
+              dA.v[i] = __ffma2_rn(gq, dt, dA.v[i]);
+              gr.v[i] = __fmul2_rn(a[j].v[i], gr.v[i]);
+            }
+            sm.s[0][t][part][my_ch] = x1.x + x1.y;
+            sm.s[1][t][part][my_ch] = x2.x + x2.y;
+            sm.s[2][t][part][my_ch] = x3.x + x3.y;
+            if (j % SET) continue;
+            // dBm, dCm of this token and the next, over the warp's channels
+            using Over = LaneSum<SET * 2 * P, 16, 1>;
+            Over::run(w, lane);
+            if ((lane & Over::copies) == 0) {
+              const int f = Over::first(lane) % (2 * P);
+              float* dst = &sm.bc[block][t + Over::first(lane) / (2 * P)][f < P ? n0 + f : N + n0 + f - P];
+#pragma unroll
+              for (int m = 0; m < Over::left; ++m) dst[m] = w[m];
             }
           }
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int tt = it + L * i, t = k * kSsmTile + tt;
-        if (!i_on || t >= p.T) continue;
-        float du = 0.f, dd = 0.f, dz = 0.f;
-        if (t < len) {
-          const float dt = sm.dt[tt][ic].x, dr = sm.dr[tt][ic], s1 = sm.s1[tt][ic];
-          du = fmaf(dt, s1, skip * dr);
-          dd = fmaf(cu[i], s1, sm.s2[tt][ic] * (1.0f / kLog2e));  // A was scaled by log2 e
-          if (p.softplus) dd *= sigmoid_fast(cx[i]);
-          if (p.z) {
-            const float sg = sigmoid_fast(cz[i]);
-            dz = cg_[i] * fmaf(skip, cu[i], sm.s3[tt][ic]) * sg * fmaf(cz[i], 1.f - sg, 1.f);
-          }
-          dskip = fmaf(dr, cu[i], dskip);
-          dbias += dd;
-        }
-        const size_t o = ob + (size_t)t * p.D;
-        static_cast<InT*>(p.du)[o] = from_f32<InT>(du);
-        static_cast<InT*>(p.ddelta)[o] = from_f32<InT>(dd);
-        if (p.z) static_cast<InT*>(p.dz)[o] = from_f32<InT>(dz);
+      if (first < last) {
+        __syncthreads();
+        asm volatile("bar.sync 1, %0;" ::"n"(S::NT) : "memory");
       }
+      if (rank == 0 && on && p.dh0) gr.store(p.dh0 + hrow);
+      if (on) {
+        float* pp = p.part_par + ((size_t)b * p.split + rank) * ((size_t)p.D * (N + 2)) + par;
 #pragma unroll
-      for (int o = tid; o < kSsmTile * 2 * N; o += NT) {
-        const int tt = o / (2 * N), i = o % (2 * N), t = k * kSsmTile + tt;
+        for (int i = 0; i < P / 2; ++i) {
+          pp[2 * i] = dA.v[i].x;
+          pp[2 * i + 1] = dA.v[i].y;
+        }
+      }
+    } else if (first < last) {
+      seek(last - 1);
+      for (int j = 0; j < AHEAD; ++j) send(last - 1 - j);
+      stage(last - 1);
+      send(last - 1 - AHEAD);
+      for (int k = last - 1; k >= first; --k) {
+        __syncthreads();
+        if (k + 1 < last)
+          finish(k + 1, sums_read);
+        else
+          sums_read();
+        if (k > first) {
+          stage(k - 1);
+          send(k - 1 - AHEAD);
+        }
+      }
+      __syncthreads();
+      finish(first, sums_read);
+      if constexpr (VEC > 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+
+    if (!recur) {
+      // tokens behind the last tile
+      if (rank == 0 && i_on) {
+        const float none[VEC] = {};
+        for (int t = n_tiles * kSsmTile + it; t < p.T; t += TS) {
+          const size_t o = ob + (size_t)t * p.D;
+          store_vec<InT, VEC>(static_cast<InT*>(p.du) + o, none);
+          store_vec<InT, VEC>(static_cast<InT*>(p.ddelta) + o, none);
+          if (p.z) store_vec<InT, VEC>(static_cast<InT*>(p.dz) + o, none);
+        }
+      }
+    }
+    // dskip, d_delta_bias: over the TS threads of a channel's items
+    __syncthreads();
+    float* red = &sm.s[0][0][0][0];  // [2][TS][CH]
+    if (!recur) {
+      store_vec<float, VEC>(red + it * CH + ic, dskip);
+      store_vec<float, VEC>(red + (TS + it) * CH + ic, dbias);
+    }
+    __syncthreads();
+    if (!recur) {
+      for (int e = tid; e < 2 * CH; e += HT) {
+        const int ch = e % CH, which = e / CH;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) s += sm.part[w][tt][i];
-        if (t < len)
-          p.part_bc[((((size_t)tile_in_group * p.B + b) * p.T + t) * p.G + g) * (2 * N) + i] = s;
+        for (int j = 0; j < TS; ++j) s += red[(which * TS + j) * CH + ch];
+        if (ch < nch)
+          p.part_par[((size_t)b * p.split + rank) * ((size_t)p.D * (N + 2)) +
+                     (size_t)p.D * (N + which) + c0 + ch] = s;
       }
-    }
-
-    // tokens behind the last tile
-    if (rank == 0 && i_on) {
-      for (int t = n_tiles * kSsmTile + it; t < p.T; t += L) {
-        const size_t o = ob + (size_t)t * p.D;
-        static_cast<InT*>(p.du)[o] = from_f32<InT>(0.f);
-        static_cast<InT*>(p.ddelta)[o] = from_f32<InT>(0.f);
-        if (p.z) static_cast<InT*>(p.dz)[o] = from_f32<InT>(0.f);
-      }
-    }
-    if (rank == 0 && on && p.dh0) store_state(p.dh0 + hrow, gr);
-
-    float* pp = p.part_par + ((size_t)b * p.split + rank) * ((size_t)p.D * (N + 2));
-    if (on) {
-      pp[par] = dA.lo.x; pp[par + 1] = dA.lo.y; pp[par + 2] = dA.hi.x; pp[par + 3] = dA.hi.y;
-    }
-    // dskip, d_delta_bias: over the L threads of a channel's items
-    __syncthreads();
-    float* red = &sm.part[0][0][0];
-    red[tid] = dskip;
-    red[NT + tid] = dbias;
-    __syncthreads();
-    if (tid < 2 * CH) {
-      const int ch = tid % CH, which = tid / CH;
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < L; ++j) s += red[which * NT + j * CH + ch];
-      if (ch < nch) pp[(size_t)p.D * (N + which) + c0 + ch] = s;
     }
     __syncthreads();
   }
