@@ -7,37 +7,46 @@
 
 namespace ttt {
 
-// 32 columns by 32 strands of rows a block; each strand adds every 32nd row.
+// COLS columns by 1024 / COLS strands of rows a block.
+template <int COLS>
 __global__ void __launch_bounds__(1024) reduce_parts_kernel(const float* part, int parts,
                                                             long long n, ReduceOut out) {
-  __shared__ float red[32][33];
-  const long long i = (long long)blockIdx.x * 32 + threadIdx.x;
+  constexpr int STRANDS = 1024 / COLS;
+  __shared__ float red[STRANDS][COLS + 1];
+  const int col = threadIdx.x % COLS, strand = threadIdx.x / COLS;
+  const long long i = (long long)blockIdx.x * COLS + col;
   float s = 0.f;
   if (i < n) {
 #pragma unroll 4
-    for (int k = threadIdx.y; k < parts; k += 32) s += part[(long long)k * n + i];
+    for (int k = strand; k < parts; k += STRANDS) s += part[(long long)k * n + i];
   }
-  red[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y != 0 || i >= n) return;
-  s = 0.f;
+  red[strand][col] = s;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) s += red[k][threadIdx.x];
+  for (int half = STRANDS / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (strand < half) red[strand][col] += red[strand + half][col];
+  }
+  if (strand != 0 || i >= n) return;
   long long o = i;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (o < out.n[k]) {
-      if (out.p[k]) out.p[k][o] = s;
+      if (out.p[k]) out.p[k][o] = red[0][col];
       return;
     }
     o -= out.n[k];
   }
 }
 
+// 8 columns a block (one sector of 32 bytes a row) where 32 would leave most SMs idle and a
+// strand long: 1184 rows of 1536, 48 blocks, took 20 us.
 int launch_reduce_parts(const float* part, int parts, long long n, const ReduceOut& out,
                         cudaStream_t stream) {
   if (n <= 0) return TTT_OK;
-  reduce_parts_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, stream>>>(part, parts, n, out);
+  if (n >= 32 * 296)
+    reduce_parts_kernel<32><<<(unsigned)((n + 31) / 32), 1024, 0, stream>>>(part, parts, n, out);
+  else
+    reduce_parts_kernel<8><<<(unsigned)((n + 7) / 8), 1024, 0, stream>>>(part, parts, n, out);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
@@ -62,6 +71,9 @@ int launch(ConvParams p, cudaStream_t s) {
   p.vecs = (int)((long long)p.H * p.d / VEC);
   const unsigned rows = p.B < kMaxGridY ? p.B : kMaxGridY;
   if constexpr (W == kForward) {
+    const long long enough = 148LL * 16 * 32 * 32;
+    p.run = (long long)p.vecs * p.B * p.T >= enough ? 32 : 8;
+    p.tiles = p.T > 0 ? (int)(((long long)p.T + p.run - 1) / p.run) : 1;
     const long long blocks = ((long long)p.tiles * p.vecs + 127) / 128;
     if (blocks > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
     ttt::conv_fwd_kernel<InT, OutT, VEC, K><<<dim3((unsigned)blocks, rows), 128, 0, s>>>(p);
@@ -90,19 +102,17 @@ int dispatch_out(const ConvParams& p, int K, unsigned mode, bool vec, cudaStream
   return vec ? dispatch_k<W, InT, float, VEC>(p, K, s) : dispatch_k<W, InT, float, 1>(p, K, s);
 }
 
-// Vectors of 16 bytes of the input (8 in the backward, whose windows and sums
-// fill the registers at 4 channels a thread).
-int vec_width(Which w, unsigned mode) { return (mode & TTT_IN_BF16) && w != kBackward ? 8 : 4; }
-
 template <Which W>
 int dispatch(const ConvParams& p, int K, unsigned mode, bool vec, cudaStream_t s) {
-  if (mode & TTT_IN_BF16)
-    return dispatch_out<W, __nv_bfloat16, W == kBackward ? 4 : 8>(p, K, mode, vec, s);
-  return dispatch_out<W, float, 4>(p, K, mode, vec, s);
+  return (mode & TTT_IN_BF16) ? dispatch_out<W, __nv_bfloat16, 4>(p, K, mode, vec, s)
+                              : dispatch_out<W, float, 4>(p, K, mode, vec, s);
 }
 
-bool can_vec(Which w, unsigned mode, int d, const Strided* ts, const void* const* ptrs, int n) {
-  const int v = vec_width(w, mode);
+// Can every row be read and written four channels at a time? (8 bytes of bf16: with 16, eight
+// channels a thread, the windows and weights leave too few warps, 170 against 108 us for
+// 2 x 32768 tokens by 2048 channels.)
+bool can_vec(int d, const Strided* ts, const void* const* ptrs, int n) {
+  const int v = 4;
   if (d % v != 0) return false;
   for (int i = 0; i < n; ++i) {
     const size_t bytes = v * ts[i].elt < 16 ? v * ts[i].elt : 16;
@@ -178,8 +188,7 @@ int ttt_conv_forward(const void* x, const float* weight, const float* bias, cons
   p.B = B; p.H = H; p.T = T; p.d = d;
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
   p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
-  p.tiles = T > 0 ? (int)(((long long)T + ttt::kConvRun - 1) / ttt::kConvRun) : 1;
-  return dispatch<kForward>(p, K, mode, can_vec(kForward, mode, d, ts, ptrs, 4),
+  return dispatch<kForward>(p, K, mode, can_vec(d, ts, ptrs, 4),
                             static_cast<cudaStream_t>(cuda_stream));
 }
 
@@ -242,7 +251,7 @@ int ttt_conv_backward(const void* x, const float* weight, const float* bias, con
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
   p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
   const int rc =
-      dispatch<kBackward>(p, K, mode, can_vec(kBackward, mode, d, ts, ptrs, 6), s);
+      dispatch<kBackward>(p, K, mode, can_vec(d, ts, ptrs, 6), s);
   if (rc != TTT_OK) return rc;
   return ttt::launch_reduce_parts(p.part, B * p.tiles, D * (K + 1),
                                   {{dweight, dbias, nullptr}, {D * K, D, 0}}, s);
@@ -278,7 +287,7 @@ int ttt_conv_step(const void* x, const float* weight, const float* bias, void* s
   p.B = B; p.H = H; p.T = 1; p.d = d;
   p.silu = (mode & TTT_CONV_SILU) ? 1 : 0;
   p.pad_zero = (mode & TTT_CONV_PAD_ZERO) ? 1 : 0;
-  return dispatch<kStep>(p, K, mode, can_vec(kStep, mode, d, ts, ptrs, 3),
+  return dispatch<kStep>(p, K, mode, can_vec(d, ts, ptrs, 3),
                          static_cast<cudaStream_t>(cuda_stream));
 }
 

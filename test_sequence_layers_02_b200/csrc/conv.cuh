@@ -33,6 +33,7 @@ struct ConvParams {
   int B, H, T, d;
   int vecs;             // vectors of VEC channels over all heads: H * d / VEC
   int tiles;            // runs of tokens (forward), blocks along the tokens (backward)
+  int run;              // tokens per run (forward)
   int silu;
   int pad_zero;         // y = 0 behind a length and in rows that are not active
 };
@@ -48,28 +49,62 @@ __device__ __forceinline__ T* row_ptr(void* p, const RowStrides& s, int b, int h
   return static_cast<T*>(p) + b * s.b + h * s.h + t * s.t + c;
 }
 
-// The VEC channels' weights, w[i][j] = weight[c + i][j]. The VEC K floats are one
-// contiguous run that starts on 16 bytes when VEC is a multiple of 4.
+// The VEC channels' weights, w[j] of tap j. The VEC K floats are one contiguous run that starts
+// on 16 bytes when VEC is 4.
 template <int VEC, int K>
-__device__ __forceinline__ void load_weights(const float* weight, int c, float (&w)[VEC][K]) {
+__device__ __forceinline__ void load_weights(const float* weight, int c, Lanes<VEC> (&w)[K]) {
   const float* p = weight + (size_t)c * K;
-  if constexpr (VEC % 4 == 0) {
-    float f[VEC * K];
+  float f[VEC * K];
+  if constexpr (VEC == 4) {
 #pragma unroll
     for (int i = 0; i < VEC * K; i += 4) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
       f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
     }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-#pragma unroll
-      for (int j = 0; j < K; ++j) w[i][j] = f[i * K + j];
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-#pragma unroll
-      for (int j = 0; j < K; ++j) w[i][j] = __ldg(p + i * K + j);
+    for (int i = 0; i < VEC * K; ++i) f[i] = __ldg(p + i);
   }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    float t[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) t[i] = f[i * K + j];
+    w[j].set(t);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> load_bias(const float* bias, int c) {
+  float t[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) t[i] = bias ? __ldg(bias + c + i) : 0.f;
+  Lanes<VEC> r;
+  r.set(t);
+  return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ Lanes<VEC> widened(const Pack<T, VEC>& x) {
+  float t[VEC];
+  x.widen(t);
+  Lanes<VEC> r;
+  r.set(t);
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Lanes<VEC> load_lanes(const T* p) {
+  float t[VEC];
+  load_vec<T, VEC>(p, t);
+  Lanes<VEC> r;
+  r.set(t);
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_lanes(T* p, const Lanes<VEC>& x) {
+  float t[VEC];
+  x.get(t);
+  store_vec<T, VEC>(p, t);
 }
 
 __device__ __forceinline__ int row_length(const int* lengths, int b, int T) {
@@ -78,96 +113,88 @@ __device__ __forceinline__ int row_length(const int* lengths, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
-constexpr int kConvRun = 16;     // tokens per thread (forward)
+constexpr int kConvBatch = 8;  // tokens loaded at a time (forward)
 
-// Linear thread index over (run, vector) in x, batch rows in y.
+// Linear thread index over (run, vector) in x, batch rows in y. p.run tokens a thread: 32 where
+// that leaves 16 warps for every SM, else 8 (short prompts, few channels).
 template <typename InT, typename OutT, int VEC, int K>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvParams p) {
+  using V = Lanes<VEC>;
   const long long idx = (long long)blockIdx.x * 128 + threadIdx.x;
   const int run = (int)(idx / p.vecs);
   if (run >= p.tiles) return;
   const int cc = (int)(idx - (long long)run * p.vecs) * VEC;  // channel over all heads
   const int h = cc / p.d, c = cc - h * p.d;
-  const int t0 = run * kConvRun;
-  float w[VEC][K], bias[VEC];
+  const int t0 = run * p.run;
+  V w[K];
   load_weights<VEC, K>(p.weight, cc, w);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) bias[i] = p.bias ? __ldg(p.bias + cc + i) : 0.f;
+  const V bias = load_bias<VEC>(p.bias, cc);
+  V zero;
+  zero.set(0.f);
 
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int len = row_length(p.lengths, b, p.T);
-    float win[K][VEC];  // inputs t-K+1 .. t
-    const InT* xp = row_ptr<InT>(p.x, p.xs, b, h, 0, c);
+    const int end = t0 + p.run < len ? t0 + p.run : len;
+    V win[4];  // the last inputs, that of token t at (t - t0) & 3: the batches turn it in place
+    const InT* xp = row_ptr<InT>(p.x, p.xs, b, h, t0, c);
+    OutT* yp = row_ptr<OutT>(p.y, p.ys, b, h, t0, c);
     if (run == 0) {
       // The first run alone reads the old state and writes the new one, so the two
       // may be the same memory.
-      float old[K - 1][VEC];
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) {
-        if (p.state)
-          load_vec<InT, VEC>(row_ptr<InT>(p.state, p.ss, b, h, j, c), old[j]);
-        else
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) old[j][i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) win[j + 1][i] = old[j][i];
-      }
+      for (int j = 0; j < K - 1; ++j)
+        win[(j - (K - 1)) & 3] =
+            p.state ? load_lanes<InT, VEC>(row_ptr<InT>(p.state, p.ss, b, h, j, c)) : zero;
       if (p.state_T) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
           const int e = len + j;  // entry of [state, x]
-          float v[VEC];
+          V v = zero;
           if (e >= K - 1) {
-            load_vec<InT, VEC>(xp + (long long)(e - (K - 1)) * p.xs.t, v);
+            v = load_lanes<InT, VEC>(xp + (long long)(e - (K - 1)) * p.xs.t);
           } else {
 #pragma unroll
             for (int q = 0; q < K - 1; ++q)
-              if (q == e)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[i] = old[q][i];
+              if (q == e) v = win[(q - (K - 1)) & 3];
           }
-          store_vec<InT, VEC>(row_ptr<InT>(p.state_T, p.so, b, h, j, c), v);
+          store_lanes<InT, VEC>(row_ptr<InT>(p.state_T, p.so, b, h, j, c), v);
         }
       }
-    } else {
-      if (t0 < len)
+    } else if (t0 < len) {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-          load_vec<InT, VEC>(xp + (long long)(t0 - (K - 1) + j) * p.xs.t, win[j + 1]);
+      for (int j = 0; j < K - 1; ++j)
+        win[(j - (K - 1)) & 3] = load_lanes<InT, VEC>(xp + (long long)(j - (K - 1)) * p.xs.t);
     }
-    OutT* yp = row_ptr<OutT>(p.y, p.ys, b, h, 0, c);
     if (p.pad_zero) {
-      const float none[VEC] = {};
-      const int end = t0 + kConvRun < p.T ? t0 + kConvRun : p.T;
-      for (int t = len > t0 ? len : t0; t < end; ++t)
-        store_vec<OutT, VEC>(yp + (long long)t * p.ys.t, none);
+      const int stop = t0 + p.run < p.T ? t0 + p.run : p.T;
+      for (int t = len > t0 ? len : t0; t < stop; ++t)
+        store_lanes<OutT, VEC>(yp + (long long)(t - t0) * p.ys.t, zero);
     }
-    constexpr int NB = VEC == 8 ? 4 : 8;  // tokens loaded at a time
-    for (int s = 0; s < kConvRun; s += NB) {
-      const int ts = t0 + s;
-      if (ts >= len) break;
-      float in[NB][VEC];
+    // the next batch is on its way while this one is worked on
+    Pack<InT, VEC> next[kConvBatch];
+    auto fetch = [&](int left) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        // behind the length: the last token again, unused
-        const int t = ts + j < len ? ts + j : len - 1;
-        load_vec<InT, VEC>(xp + (long long)t * p.xs.t, in[j]);
+      for (int j = 0; j < kConvBatch; ++j)
+        if (j < left) next[j] = *reinterpret_cast<const Pack<InT, VEC>*>(xp + (long long)j * p.xs.t);
+      xp += kConvBatch * p.xs.t;
+    };
+    fetch(end - t0);
+    for (int t = t0; t < end; t += kConvBatch) {
+      const int left = end - t;
+      Pack<InT, VEC> in[kConvBatch];
+#pragma unroll
+      for (int j = 0; j < kConvBatch; ++j) in[j] = next[j];
+      fetch(left - kConvBatch);
+#pragma unroll
+      for (int j = 0; j < kConvBatch; ++j) {
+        win[j & 3] = widened<InT, VEC>(in[j]);
+        V a = bias;
+#pragma unroll
+        for (int q = 0; q < K; ++q) a.fma(w[q], win[(j - (K - 1) + q) & 3]);
+        if (p.silu) a.mul(a.sigmoid());
+        if (j < left) store_lanes<OutT, VEC>(yp + (long long)j * p.ys.t, a);
       }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        float out[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-          for (int q = 0; q < K - 1; ++q) win[q][i] = win[q + 1][i];
-          win[K - 1][i] = in[j][i];
-          float a = bias[i];
-#pragma unroll
-          for (int q = 0; q < K; ++q) a = fmaf(w[i][q], win[q][i], a);
-          out[i] = p.silu ? a * sigmoid_fast(a) : a;
-        }
-        if (ts + j < len) store_vec<OutT, VEC>(yp + (long long)(ts + j) * p.ys.t, out);
-      }
+      yp += kConvBatch * p.ys.t;
     }
   }
 }
@@ -183,7 +210,8 @@ constexpr int kConvSeg = 32;
 constexpr int kConvSegs = 8;
 
 template <typename InT, typename OutT, int VEC, int K>
-__global__ void __launch_bounds__(32 * kConvSegs) conv_bwd_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(32 * kConvSegs, 2) conv_bwd_kernel(const ConvParams p) {
+  using V = Lanes<VEC>;
   __shared__ float red[kConvSegs][32][VEC * (K + 1) + 1];
   const int lane = threadIdx.x, seg = threadIdx.y;
   const int vec = blockIdx.x * 32 + lane;
@@ -193,126 +221,138 @@ __global__ void __launch_bounds__(32 * kConvSegs) conv_bwd_kernel(const ConvPara
   const int tile = blockIdx.y;
   const int t0 = (tile * kConvSegs + seg) * kConvSeg;
   const long long D = (long long)p.H * p.d;
-  float w[VEC][K], bias[VEC];
+  V w[K], zero;
   load_weights<VEC, K>(p.weight, cc, w);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) bias[i] = p.bias ? __ldg(p.bias + cc + i) : 0.f;
+  const V bias = load_bias<VEC>(p.bias, cc);
+  zero.set(0.f);
   const RowStrides dxs = {(long long)p.H * p.T * p.d, (long long)p.T * p.d, p.d};
   const RowStrides dss = {(long long)p.H * (K - 1) * p.d, (long long)(K - 1) * p.d, p.d};
 
   for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
     const int len = row_length(p.lengths, b, p.T);
-    float dw[VEC][K], db[VEC];
+    V dw[K], db = zero;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      db[i] = 0.f;
-#pragma unroll
-      for (int q = 0; q < K; ++q) dw[i][q] = 0.f;
-    }
+    for (int q = 0; q < K; ++q) dw[q] = zero;
     if (on && (t0 < p.T || (tile == 0 && seg == 0))) {
-      const InT* xp = row_ptr<InT>(p.x, p.xs, b, h, 0, c);
-      const OutT* gp = row_ptr<OutT>(const_cast<const void*>(p.y), p.ys, b, h, 0, c);
-      InT* dxp = row_ptr<InT>(p.dx, dxs, b, h, 0, c);
+      const InT* xp = row_ptr<InT>(p.x, p.xs, b, h, t0, c);
+      const OutT* gp = row_ptr<OutT>(const_cast<const void*>(p.y), p.ys, b, h, t0, c);
+      InT* dxp = row_ptr<InT>(p.dx, dxs, b, h, t0, c);
       const int end = t0 + kConvSeg < p.T ? t0 + kConvSeg : p.T;  // dx written up to here
       const bool first = t0 == 0;
       // inputs t0-K+1 .. t0-1 (0 behind the length, where nothing uses them)
-      float win[K][VEC], dwin[K][VEC];
+      V win[4], dwin[4];  // of token t at (t - t0) & 3
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         const int t = t0 - (K - 1) + j;
-        if (t >= 0 && t < len) {
-          load_vec<InT, VEC>(xp + (long long)t * p.xs.t, win[j + 1]);
-        } else if (t < 0 && p.state) {
-          load_vec<InT, VEC>(row_ptr<InT>(p.state, p.ss, b, h, t + K - 1, c), win[j + 1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) win[j + 1][i] = 0.f;
-        }
+        if (t >= 0 && t < len)
+          win[(j - (K - 1)) & 3] = load_lanes<InT, VEC>(xp + (long long)(j - (K - 1)) * p.xs.t);
+        else if (t < 0 && p.state)
+          win[(j - (K - 1)) & 3] =
+              load_lanes<InT, VEC>(row_ptr<InT>(p.state, p.ss, b, h, t + K - 1, c));
+        else
+          win[(j - (K - 1)) & 3] = zero;
       }
 #pragma unroll
-      for (int q = 0; q < K; ++q)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dwin[q][i] = 0.f;
+      for (int q = 0; q < 4; ++q) dwin[q] = zero;
 
-      // one token: d(pre_t) into dwin (0 behind the length), its weight sums, and
-      // dx at t - K + 1
-      auto token = [&](int t, const float (&xin)[VEC], const float (&gin)[VEC]) {
+      // Token t = ts + j: d(pre_t) into dwin, its weight sums, and dx at t - K + 1. `inner`: t lies
+      // in the segment and in the length, and t - K + 1 in the segment; else what lies
+      // behind the length is 0, and a later segment's token leaves its sums to it.
+      auto token = [&](int t, int j, const V& xin, V g, bool inner) {
+        win[j & 3] = xin;
+        if (p.silu) {
+          V a = bias;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-          for (int q = 0; q < K - 1; ++q) {
-            win[q][i] = win[q + 1][i];
-            dwin[q][i] = dwin[q + 1][i];
-          }
-          win[K - 1][i] = xin[i];
-          float g = gin[i];
-          if (p.silu) {
-            float a = bias[i];
-#pragma unroll
-            for (int q = 0; q < K; ++q) a = fmaf(w[i][q], win[q][i], a);
-            const float sg = sigmoid_fast(a);
-            g *= sg * fmaf(a, 1.f - sg, 1.f);
-          }
-          if (t >= len) g = 0.f;
-          dwin[K - 1][i] = g;
-          if (t >= end) g = 0.f;  // a later segment's token: its sums are there
-          db[i] += g;
-#pragma unroll
-          for (int q = 0; q < K; ++q) dw[i][q] = fmaf(g, win[q][i], dw[i][q]);
+          for (int q = 0; q < K; ++q) a.fma(w[q], win[(j - (K - 1) + q) & 3]);
+          const V sg = a.sigmoid();
+          // SiLU'(a) = s (1 + a (1 - s)) = s + a s - (a s) s
+          a.mul(sg);
+          V d = sg;
+          d.add(a);
+          d.fma_minus(a, sg);
+          g.mul(d);
         }
+        if (!inner && t >= len) g = zero;
+        dwin[j & 3] = g;
+        if (!inner && t >= end) g = zero;
+        db.add(g);
+#pragma unroll
+        for (int q = 0; q < K; ++q) dw[q].fma(g, win[(j - (K - 1) + q) & 3]);
         const int e = t - (K - 1);  // the input whose gradient is complete now
-        if (e >= end || (e < t0 && !(first && e < 0))) return;
-        float out[VEC];
+        if (!inner && (e >= end || (e < t0 && !(first && e < 0)))) return;
+        V out = w[K - 1];
+        out.mul(dwin[(j - (K - 1)) & 3]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          out[i] = 0.f;
-#pragma unroll
-          for (int q = 0; q < K; ++q) out[i] = fmaf(w[i][K - 1 - q], dwin[q][i], out[i]);
+        for (int q = 1; q < K; ++q) out.fma(w[K - 1 - q], dwin[(j - (K - 1) + q) & 3]);
+        if (inner) {
+          store_lanes<InT, VEC>(dxp + (long long)(e - t0) * p.d, out);
+          return;
         }
         const int js = e + (K - 1) - len;  // its place in state_T, if it has one
-        if (p.dstate_T && js >= 0 && js < K - 1 && e < len) {
-          float ds[VEC];
-          load_vec<InT, VEC>(row_ptr<InT>(p.dstate_T, dss, b, h, js, c), ds);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) out[i] += ds[i];
-        }
+        if (p.dstate_T && js >= 0 && js < K - 1 && e < len)
+          out.add(load_lanes<InT, VEC>(row_ptr<InT>(p.dstate_T, dss, b, h, js, c)));
         if (e >= 0) {
-          if (e >= len)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) out[i] = 0.f;
-          store_vec<InT, VEC>(dxp + (long long)e * p.d, out);
+          if (e >= len) out = zero;
+          store_lanes<InT, VEC>(dxp + (long long)(e - t0) * p.d, out);
         } else if (p.dstate) {
-          store_vec<InT, VEC>(row_ptr<InT>(p.dstate, dss, b, h, e + K - 1, c), out);
+          store_lanes<InT, VEC>(row_ptr<InT>(p.dstate, dss, b, h, e + K - 1, c), out);
         }
       };
 
       const int stop = end + K - 1;
-      constexpr int NB = 4;  // tokens loaded at a time
-      for (int ts = t0; ts < stop; ts += NB) {
-        float xin[NB][VEC], gin[NB][VEC];
-        if (ts < len) {
+      constexpr int NB = 4;  // tokens loaded at a time; the next ones while these are worked on
+      Pack<InT, VEC> xnext[NB];
+      Pack<OutT, VEC> gnext[NB];
+      auto fetch = [&](int left) {
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const int t = ts + j < len ? ts + j : len - 1;  // behind the length: unused
-            load_vec<InT, VEC>(xp + (long long)t * p.xs.t, xin[j]);
-            load_vec<OutT, VEC>(gp + (long long)t * p.ys.t, gin[j]);
+        for (int j = 0; j < NB; ++j) {
+          if (j < left) {
+            xnext[j] = *reinterpret_cast<const Pack<InT, VEC>*>(xp + (long long)j * p.xs.t);
+            gnext[j] = *reinterpret_cast<const Pack<OutT, VEC>*>(gp + (long long)j * p.ys.t);
+          } else {
+            xnext[j] = {};
+            gnext[j] = {};
           }
+        }
+        xp += NB * p.xs.t;
+        gp += NB * p.ys.t;
+      };
+      const int seen = stop < len ? stop : len;   // no token is needed from here on
+      const int inner = end < len ? end : len;
+      fetch(seen - t0);
+      for (int ts = t0; ts < stop; ts += NB) {
+        Pack<InT, VEC> xin[NB];
+        Pack<OutT, VEC> gin[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          xin[j] = xnext[j];
+          gin[j] = gnext[j];
+        }
+        fetch(seen - ts - NB);
+        if (ts > t0 && ts + NB <= inner) {
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            token(ts + j, j, widened<InT, VEC>(xin[j]), widened<OutT, VEC>(gin[j]), true);
         } else {
 #pragma unroll
           for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) xin[j][i] = gin[j][i] = 0.f;
+            token(ts + j, j, widened<InT, VEC>(xin[j]), widened<OutT, VEC>(gin[j]), false);
         }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) token(ts + j, xin[j], gin[j]);
       }
     }
     // partial sums of the block: over its segments in order
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int q = 0; q < K; ++q) {
+      float f[VEC];
+      dw[q].get(f);
 #pragma unroll
-      for (int q = 0; q < K; ++q) red[seg][lane][i * K + q] = dw[i][q];
-      red[seg][lane][VEC * K + i] = db[i];
+      for (int i = 0; i < VEC; ++i) red[seg][lane][i * K + q] = f[i];
+    }
+    {
+      float f[VEC];
+      db.get(f);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) red[seg][lane][VEC * K + i] = f[i];
     }
     __syncthreads();
     float* part = p.part + ((long long)b * p.tiles + tile) * (D * (K + 1));
@@ -336,36 +376,35 @@ __global__ void __launch_bounds__(32 * kConvSegs) conv_bwd_kernel(const ConvPara
 // ---- one token ----
 template <typename InT, typename OutT, int VEC, int K>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
+  using V = Lanes<VEC>;
   const int vec = blockIdx.x * 128 + threadIdx.x;
   if (vec >= p.vecs) return;
   const int cc = vec * VEC;
   const int h = cc / p.d, c = cc - h * p.d;
-  float w[VEC][K];
+  V w[K];
   load_weights<VEC, K>(p.weight, cc, w);
+  const V bias = load_bias<VEC>(p.bias, cc);
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    float win[K][VEC], out[VEC];
+    OutT* yp = row_ptr<OutT>(p.y, p.ys, b, h, 0, c);
     if (p.active && !p.active[b]) {
       if (p.pad_zero) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) out[i] = 0.f;
-        store_vec<OutT, VEC>(row_ptr<OutT>(p.y, p.ys, b, h, 0, c), out);
+        V zero;
+        zero.set(0.f);
+        store_lanes<OutT, VEC>(yp, zero);
       }
       continue;
     }
+    V win[K], a = bias;
     InT* st = row_ptr<InT>(p.state_T, p.ss, b, h, 0, c);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load_vec<InT, VEC>(st + j * p.ss.t, win[j]);
-    load_vec<InT, VEC>(row_ptr<InT>(p.x, p.xs, b, h, 0, c), win[K - 1]);
+    for (int j = 0; j < K - 1; ++j) win[j] = load_lanes<InT, VEC>(st + j * p.ss.t);
+    win[K - 1] = load_lanes<InT, VEC>(row_ptr<InT>(p.x, p.xs, b, h, 0, c));
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float a = p.bias ? __ldg(p.bias + cc + i) : 0.f;
+    for (int q = 0; q < K; ++q) a.fma(w[q], win[q]);
+    if (p.silu) a.mul(a.sigmoid());
+    store_lanes<OutT, VEC>(yp, a);
 #pragma unroll
-      for (int q = 0; q < K; ++q) a = fmaf(w[i][q], win[q][i], a);
-      out[i] = p.silu ? a * sigmoid_fast(a) : a;
-    }
-    store_vec<OutT, VEC>(row_ptr<OutT>(p.y, p.ys, b, h, 0, c), out);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) store_vec<InT, VEC>(st + j * p.ss.t, win[j + 1]);
+    for (int j = 0; j < K - 1; ++j) store_lanes<InT, VEC>(st + j * p.ss.t, win[j + 1]);
   }
 }
 

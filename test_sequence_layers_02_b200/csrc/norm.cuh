@@ -3,7 +3,7 @@
 // One read of x and the residual, one write of s and y: HBM bounds it. A row stays in
 // registers between its sum of squares and its output. In the vector form a
 // lane holds VPT groups of 8 neighbouring columns and a row takes W warps; rows of
-// up to 2048 columns fit one warp, which then needs no barrier at all, and four
+// up to 1024 columns fit one warp, which then needs no barrier at all, and four
 // such rows share a CTA. Rows whose pointers or strides are off 16 bytes, or
 // with D not a multiple of 8, take the same kernel with single columns.
 #pragma once
@@ -175,17 +175,18 @@ __global__ void norm_fwd_kernel(const NormParams p) {
       // at least the smallest normal number: a row of zeros stays dividable
       const float scale = fmaxf(amax[v] / 448.f, 1.17549435e-38f);
       if (p.group128 ? c % 128 == 0 : c == 0) sc[p.group128 ? c / 128 : 0] = scale;
-      unsigned char q[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        q[i] = __nv_cvt_float_to_fp8(s[v][i] / scale, __NV_SATFINITE, __NV_E4M3);
+      // Times the reciprocal in place of 8 divisions: a quotient moves by 2^-23 of itself, which
+      // reaches a code only that near to the middle between two.
+      const float inv = 1.0f / scale;
       if constexpr (VEC == 8) {
-        uint2 o;
-        o.x = q[0] | q[1] << 8 | q[2] << 16 | (uint32_t)q[3] << 24;
-        o.y = q[4] | q[5] << 8 | q[6] << 16 | (uint32_t)q[7] << 24;
-        *reinterpret_cast<uint2*>(yp + c) = o;
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[i] = __nv_cvt_float2_to_fp8x2(make_float2(s[v][2 * i] * inv, s[v][2 * i + 1] * inv),
+                                          __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(yp + c) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
       } else {
-        yp[c] = q[0];
+        yp[c] = __nv_cvt_float_to_fp8(s[v][0] * inv, __NV_SATFINITE, __NV_E4M3);
       }
     }
   }
@@ -196,7 +197,7 @@ __global__ void norm_fwd_kernel(const NormParams p) {
 // row of partial sums per CTA and are added by reduce_parts_kernel. MAXT bounds the
 // CTA (a row of 16384 columns takes 1024 threads, which leaves 64 registers each).
 template <typename GT, typename ST, int VEC, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_bwd_kernel(const NormBwdParams p) {
   __shared__ float2 red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float w[VPT][VEC], dw[VPT][VEC];
@@ -207,24 +208,37 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdParams p) {
     for (int i = 0; i < VEC; ++i) w[v][i] = dw[v][i] = 0.f;
     if (c < p.D) load_vec<float, VEC>(p.weight + c, w[v]);
   }
-  int buf = 0;
-  for (long long row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
+  // The next row's numbers are on their way while this one's are worked on.
+  Pack<GT, VEC> gn[VPT];
+  Pack<ST, VEC> sn[VPT], en[VPT];
+  auto fetch = [&](long long row) {
     const GT* gp = static_cast<const GT*>(p.dy) + row * p.dy_ld;
     const ST* sp = static_cast<const ST*>(p.s) + row * p.s_ld;
     const ST* ep = static_cast<const ST*>(p.ds) + row * p.ds_ld;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = norm_column<VEC, VPT>(warp, lane, v);
+      gn[v] = {};
+      sn[v] = en[v] = {};
+      if (c < p.D) {
+        gn[v] = *reinterpret_cast<const Pack<GT, VEC>*>(gp + c);
+        sn[v] = *reinterpret_cast<const Pack<ST, VEC>*>(sp + c);
+        if (p.ds) en[v] = *reinterpret_cast<const Pack<ST, VEC>*>(ep + c);
+      }
+    }
+  };
+  int buf = 0;
+  if (blockIdx.x < p.M) fetch(blockIdx.x);
+  for (long long row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
     ST* op = static_cast<ST*>(p.dx) + row * p.dx_ld;
     float g[VPT][VEC], s[VPT][VEC], e[VPT][VEC];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = norm_column<VEC, VPT>(warp, lane, v);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) g[v][i] = s[v][i] = e[v][i] = 0.f;
-      if (c < p.D) {
-        load_vec<GT, VEC>(gp + c, g[v]);
-        load_vec<ST, VEC>(sp + c, s[v]);
-        if (p.ds) load_vec<ST, VEC>(ep + c, e[v]);
-      }
+      gn[v].widen(g[v]);
+      sn[v].widen(s[v]);
+      en[v].widen(e[v]);
     }
+    if (row + gridDim.x < p.M) fetch(row + gridDim.x);
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v)

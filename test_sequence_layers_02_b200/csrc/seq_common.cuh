@@ -95,18 +95,125 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
   }
 }
 
-// Sum of `parts` rows of n floats, in row order within each of 32 interleaved
-// strands and then over the strands: the same bits on every call. Column i goes
-// to the segment that holds it (up to three outputs laid end to end); a null
-// output is skipped.
+// VEC neighbouring elements of a row as they are in memory, in as few registers.
+template <typename T, int VEC>
+struct Pack;
+template <>
+struct Pack<float, 1> {
+  float v;
+  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = v; }
+};
+template <>
+struct Pack<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void widen(float (&o)[4]) const {
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+  unsigned short v;
+  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
+};
+template <>
+struct Pack<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void widen(float (&o)[4]) const {
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+template <>
+struct Pack<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void widen(float (&o)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(w[i] << 16);
+      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Pack<float, 8> {
+  float4 v, w;
+  __device__ __forceinline__ void widen(float (&o)[8]) const {
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    o[4] = w.x; o[5] = w.y; o[6] = w.z; o[7] = w.w;
+  }
+};
+
+// VEC neighbouring channels in fp32, in pairs for the paired instructions where there are
+// pairs (half the issue slots).
+template <int VEC>
+struct Lanes {
+  float2 v[VEC / 2];
+  __device__ __forceinline__ void set(float x) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[i] = make_float2(x, x);
+  }
+  __device__ __forceinline__ void set(const float (&x)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+  }
+  __device__ __forceinline__ void get(float (&x)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) { x[2 * i] = v[i].x; x[2 * i + 1] = v[i].y; }
+  }
+  // this += a b
+  __device__ __forceinline__ void fma(const Lanes& a, const Lanes& b) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[i] = __ffma2_rn(a.v[i], b.v[i], v[i]);
+  }
+  __device__ __forceinline__ void mul(const Lanes& a) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[i] = __fmul2_rn(v[i], a.v[i]);
+  }
+  __device__ __forceinline__ void add(const Lanes& a) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v[i] = __fadd2_rn(v[i], a.v[i]);
+  }
+  // this -= a b
+  __device__ __forceinline__ void fma_minus(const Lanes& a, const Lanes& b) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i)
+      v[i] = __ffma2_rn(make_float2(-a.v[i].x, -a.v[i].y), b.v[i], v[i]);
+  }
+  // 1 / (1 + exp(-this)), as sigmoid_fast
+  __device__ __forceinline__ Lanes sigmoid() const {
+    Lanes r;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float2 x = __fmul2_rn(v[i], make_float2(-kLog2e, -kLog2e));
+      const float2 d = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+      r.v[i] = make_float2(rcp(d.x), rcp(d.y));
+    }
+    return r;
+  }
+};
+template <>
+struct Lanes<1> {
+  float v;
+  __device__ __forceinline__ void set(float x) { v = x; }
+  __device__ __forceinline__ void set(const float (&x)[1]) { v = x[0]; }
+  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = v; }
+  __device__ __forceinline__ void fma(const Lanes& a, const Lanes& b) { v = fmaf(a.v, b.v, v); }
+  __device__ __forceinline__ void fma_minus(const Lanes& a, const Lanes& b) { v = fmaf(-a.v, b.v, v); }
+  __device__ __forceinline__ void mul(const Lanes& a) { v *= a.v; }
+  __device__ __forceinline__ void add(const Lanes& a) { v += a.v; }
+  __device__ __forceinline__ Lanes sigmoid() const { return {sigmoid_fast(v)}; }
+};
+
+// Sum of `parts` rows of n floats in an order that `parts` and n fix: the same bits on every
+// call. Column i goes to the segment that holds it (up to three outputs laid end to end); a
+// null output is skipped.
 struct ReduceOut {
   float* p[3];
   long long n[3];
 };
 
-__global__ void reduce_parts_kernel(const float* part, int parts, long long n, ReduceOut out);
-
-// Enqueue it (defined in conv.cu).
+// Defined in conv.cu.
 int launch_reduce_parts(const float* part, int parts, long long n, const ReduceOut& out,
                         cudaStream_t stream);
 

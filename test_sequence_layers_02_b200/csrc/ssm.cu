@@ -114,12 +114,23 @@ int launch_bwd(const SsmParams& p, cudaStream_t s) {
   return p.vec ? launch_bwd_as<N, P, InT, float, 4>(p, s) : launch_bwd_as<N, P, InT, float, 1>(p, s);
 }
 
+// Four batch rows a thread once that still leaves 16 warps for every SM.
+template <int L, typename InT, int VEC>
+int launch_step_as(const SsmParams& p, cudaStream_t s) {
+  const long long blocks = ((long long)p.D * L + 255) / 256;
+  const bool four = blocks * (p.B / 2) >= 2LL * sm_count();
+  const int rows = four ? (p.B + 2 - 1) / 2 : p.B;
+  const dim3 grid((unsigned)blocks, rows < kMaxGridY ? rows : kMaxGridY);
+  if (four)
+    ttt::ssm_step_kernel<L, InT, VEC, 2><<<grid, 256, 0, s>>>(p);
+  else
+    ttt::ssm_step_kernel<L, InT, VEC, 1><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
 template <int L, typename InT>
 int launch_step(const SsmParams& p, cudaStream_t s) {
-  const long long blocks = ((long long)p.D * L + 255) / 256;
-  ttt::ssm_step_kernel<L, InT>
-      <<<dim3((unsigned)blocks, p.B < kMaxGridY ? p.B : kMaxGridY), 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return p.vec ? launch_step_as<L, InT, 4>(p, s) : launch_step_as<L, InT, 1>(p, s);
 }
 
 enum Which { kForward, kBackward, kStep };
@@ -361,6 +372,8 @@ int ttt_ssm_step(const void* u, const void* delta, const float* A, const void* B
   p.softplus = (mode & TTT_SSM_SOFTPLUS) ? 1 : 0;
   p.out_bf16 = (mode & TTT_OUT_BF16) ? 1 : 0;
   p.pad_zero = (mode & TTT_SSM_PAD_ZERO) ? 1 : 0;
+  p.vec = !misaligned_to(Bm, 4 * ie) && !misaligned_to(Cm, 4 * ie) &&
+          (p.Bm_b | p.Bm_g | p.Cm_b | p.Cm_g) % 4 == 0;
   return dispatch<kStep>(p, N, mode, static_cast<cudaStream_t>(cuda_stream));
 }
 

@@ -154,35 +154,6 @@ struct States {
   }
 };
 
-// VEC neighbouring elements of a row as they are in memory, in as few registers.
-template <typename T, int VEC>
-struct Pack;
-template <>
-struct Pack<float, 1> {
-  float v;
-  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = v; }
-};
-template <>
-struct Pack<float, 4> {
-  float4 v;
-  __device__ __forceinline__ void widen(float (&o)[4]) const {
-    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-  }
-};
-template <>
-struct Pack<__nv_bfloat16, 1> {
-  unsigned short v;
-  __device__ __forceinline__ void widen(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
-};
-template <>
-struct Pack<__nv_bfloat16, 4> {
-  uint2 v;
-  __device__ __forceinline__ void widen(float (&o)[4]) const {
-    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
-    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-};
-
 // Copy BYTES (4, 8 or 16) to shared memory without a register; `have` false: zeros.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool have) {
@@ -287,7 +258,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
 
     // ---- around the recurrence ----
     // Running pointers to a helper's items and packs of the tile to be fetched next.
-    const InT *up, *dp, *zp, *Bp, *Cp;
+    const InT *up = nullptr, *dp = nullptr, *zp = nullptr, *Bp = nullptr, *Cp = nullptr;
     const bool bc_on = S::BCQ % HT == 0 || tid < S::BCQ;
     constexpr int BROW = N / VEC;          // packs of a token
     constexpr int BS = HT / BROW;          // tokens between a helper's packs
@@ -433,8 +404,8 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
         }
       }
     };
-    __nv_bfloat16* y16;
-    float* y32;
+    __nv_bfloat16* y16 = nullptr;
+    float* y32 = nullptr;
     // The outputs of tile k, from the warps' parts.
     auto write_out = [&](int k) {
       const int h = k & 1;
@@ -639,59 +610,74 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
 }
 
 // ---- one token ----
-// L lanes a channel; the state is read once and written once (HBM bound: 8 N
-// bytes a channel against a few of input).
-template <int L, typename InT>
+// L lanes a channel, a float4 of its state each; the state is read once and written once (HBM
+// bound: 8 N bytes a channel against a few of input). A thread takes the same states of ROWS
+// batch rows, whose loads it has on their way together, with one read of the parameters.
+template <int L, typename InT, int VEC, int ROWS>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
   constexpr int N = 4 * L;
   const int c = (blockIdx.x * 256 + threadIdx.x) / L;
   const int n0 = (threadIdx.x % L) * 4;
-  // whole channels leave, but their lanes stay for the shuffles
+  // lanes of channels that are not there stay for the shuffles
   const bool on = c < p.D;
   const int cc = on ? c : p.D - 1;
   const int g = cc / p.per_group;
   const size_t par = (size_t)cc * N + n0;
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const long long o = b * p.y_b + cc;
-    auto put = [&](float r) {
-      if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(r);
-      else
-        static_cast<float*>(p.y)[o] = r;
-    };
-    if (p.active && !p.active[b]) {
-      if (p.pad_zero && on && threadIdx.x % L == 0) put(0.f);
-      continue;
-    }
-    float* hp = p.h_T + (size_t)b * p.D * N + par;
-    State4 h = load_state(hp), A = load_state(p.A + par);
-    float Bv[4], Cv[4];
-    const InT* Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g + n0;
-    const InT* Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g + n0;
+  const State4 A = load_state(p.A + par);
+  const float bias = p.delta_bias ? p.delta_bias[cc] : 0.f;
+  const float skip = p.skip ? p.skip[cc] : 0.f;
+  for (int b0 = blockIdx.y * ROWS; b0 < p.B; b0 += gridDim.y * ROWS) {
+    State4 h[ROWS];
+    float Bv[ROWS][4], Cv[ROWS][4], u[ROWS], dt[ROWS], z[ROWS];
+    bool live[ROWS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Bv[j] = to_f32(Bp[j]);
-      Cv[j] = to_f32(Cp[j]);
-    }
-    const float u = to_f32(static_cast<const InT*>(p.u)[b * p.u_b + cc]);
-    float dt = to_f32(static_cast<const InT*>(p.delta)[b * p.d_b + cc]);
-    const float z = p.z ? to_f32(static_cast<const InT*>(p.z)[b * p.z_b + cc]) : 0.f;
-    if (p.delta_bias) dt += p.delta_bias[cc];
-    if (p.softplus) dt = softplus(dt);
-    const float x = dt * kLog2e, dtu = dt * u;
-    h.lo.x = fmaf(ex2(x * A.lo.x), h.lo.x, dtu * Bv[0]);
-    h.lo.y = fmaf(ex2(x * A.lo.y), h.lo.y, dtu * Bv[1]);
-    h.hi.x = fmaf(ex2(x * A.hi.x), h.hi.x, dtu * Bv[2]);
-    h.hi.y = fmaf(ex2(x * A.hi.y), h.hi.y, dtu * Bv[3]);
-    float r = fmaf(Cv[0], h.lo.x, Cv[1] * h.lo.y) + fmaf(Cv[2], h.hi.x, Cv[3] * h.hi.y);
+    for (int r = 0; r < ROWS; ++r) {
+      const int b = min(b0 + r, p.B - 1);
+      live[r] = b0 + r < p.B && (!p.active || p.active[b]);
+      // Also for rows that are not active: their loads would wait for the flag, and only the
+      // stores matter.
+      h[r] = load_state(p.h_T + (size_t)b * p.D * N + par);
+      const InT* Bp = static_cast<const InT*>(p.Bm) + b * p.Bm_b + g * p.Bm_g + n0;
+      const InT* Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g + n0;
+      if constexpr (VEC == 4) {
+        load_vec<InT, 4>(Bp, Bv[r]);
+        load_vec<InT, 4>(Cp, Cv[r]);
+      } else {
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
-    if (!on) continue;
-    store_state(hp, h);
-    if (threadIdx.x % L == 0) {
-      if (p.skip) r = fmaf(p.skip[cc], u, r);
-      if (p.z) r *= z * sigmoid_fast(z);
-      put(r);
+        for (int j = 0; j < 4; ++j) {
+          Bv[r][j] = to_f32(Bp[j]);
+          Cv[r][j] = to_f32(Cp[j]);
+        }
+      }
+      u[r] = to_f32(static_cast<const InT*>(p.u)[b * p.u_b + cc]);
+      dt[r] = to_f32(static_cast<const InT*>(p.delta)[b * p.d_b + cc]);
+      z[r] = p.z ? to_f32(static_cast<const InT*>(p.z)[b * p.z_b + cc]) : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int b = min(b0 + r, p.B - 1);
+      float d = dt[r] + bias;
+      if (p.softplus) d = softplus(d);
+      const float x = d * kLog2e, dtu = d * u[r];
+      State4& s = h[r];
+      s.lo.x = fmaf(ex2(x * A.lo.x), s.lo.x, dtu * Bv[r][0]);
+      s.lo.y = fmaf(ex2(x * A.lo.y), s.lo.y, dtu * Bv[r][1]);
+      s.hi.x = fmaf(ex2(x * A.hi.x), s.hi.x, dtu * Bv[r][2]);
+      s.hi.y = fmaf(ex2(x * A.hi.y), s.hi.y, dtu * Bv[r][3]);
+      float y = fmaf(Cv[r][0], s.lo.x, Cv[r][1] * s.lo.y) + fmaf(Cv[r][2], s.hi.x, Cv[r][3] * s.hi.y);
+#pragma unroll
+      for (int off = L / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+      if (live[r] && on) store_state(p.h_T + (size_t)b * p.D * N + par, s);
+      y = fmaf(skip, u[r], y);
+      if (p.z) y *= z[r] * sigmoid_fast(z[r]);
+      if (on && b0 + r < p.B && threadIdx.x % L == 0 && (live[r] || p.pad_zero)) {
+        if (!live[r]) y = 0.f;
+        const long long o = b * p.y_b + cc;
+        if (p.out_bf16)
+          static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
+        else
+          static_cast<float*>(p.y)[o] = y;
+      }
     }
   }
 }

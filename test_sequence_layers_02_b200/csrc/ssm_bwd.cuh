@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
     const int first = min(n_tiles, rank * per), last = min(n_tiles, first + per);
 
     // ---- around the recurrence ----
-    const InT *up, *dp, *zp, *Bp, *Cp;
-    const OutT* gp;
+    const InT *up = nullptr, *dp = nullptr, *zp = nullptr, *Bp = nullptr, *Cp = nullptr;
+    const OutT* gp = nullptr;
     const bool bc_on = S::BCQ % HT == 0 || tid < S::BCQ;
     constexpr int BROW = N / VEC, BS = HT / BROW;
     const int bt = tid / BROW, bn = tid % BROW * VEC;
