@@ -84,6 +84,14 @@ def out_dtype_of(out_dtype, y, default: torch.dtype) -> torch.dtype:
     return out_dtype
 
 
+def like(x: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """A contiguous tensor of x's shape and device, not initialised (``empty_like``, where it gives
+    that, takes a third of ``empty``'s time)."""
+    if not x.is_contiguous():
+        return torch.empty(x.shape, dtype=dtype, device=x.device)
+    return torch.empty_like(x) if x.dtype is dtype else torch.empty_like(x, dtype=dtype)
+
+
 def _contiguous_strides(shape):
     s, step = [], 1
     for n in reversed(shape):

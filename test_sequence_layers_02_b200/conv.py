@@ -18,8 +18,8 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
-                       raise_for, strides_of, workspace_of)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+                       out_dtype_of, raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 CONV_SILU = 1 << 16
@@ -81,10 +81,11 @@ def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths
     mode = _mode(in_dtype, out_dtype, silu, y is None)
     with On(dev, stream, (x, weight, bias, state, lengths, y, state_T)) as s:
         if y is None:
-            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+            y = like(x, out_dtype)
         yp = check("y", y, x.shape, out_dtype, dev)
         if state_T is None:
-            state_T = torch.empty(s_shape, dtype=in_dtype, device=dev)
+            state_T = (torch.empty(s_shape, dtype=in_dtype, device=dev) if state is None
+                       else like(state, in_dtype))
         tp = check("state_T", state_T, s_shape, in_dtype, dev)
         o = _OUTER[x.dim()]
         st = strides_of(12, (x, o), (y, o), (s_shape if state is None else state, o), (state_T, o))
@@ -120,7 +121,7 @@ def causal_conv_backward(x, weight, bias, dy, dstate_T=None, *, silu: bool = Fal
     st = strides_of(9, (x, o), (dy, o), (s_shape if state is None else state, o))
     with On(dev, stream, (x, weight, bias, dy, dstate_T, state, lengths, workspace)) as s:
         workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(B, H, T, d, K), dev)
-        dx = torch.empty(x.shape, dtype=in_dtype, device=dev)
+        dx = like(x, in_dtype)
         dstate = torch.empty(s_shape, dtype=in_dtype, device=dev)
         dweight = torch.empty_like(weight)
         dbias = None if bias is None else torch.empty_like(bias)
@@ -151,7 +152,7 @@ def causal_conv_step(x, weight, bias, state, *, silu: bool = False, active=None,
     mode = _mode(in_dtype, out_dtype, silu, y is None)
     with On(dev, stream, (x, weight, bias, state, active, y)) as s:
         if y is None:
-            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+            y = like(x, out_dtype)
         yp = check("y", y, x.shape, out_dtype, dev)
         o = (0, 1) if x.dim() == 3 else (0, 0)
         st = strides_of(7, (x, o), (y, o), (state, _OUTER[state.dim()]))

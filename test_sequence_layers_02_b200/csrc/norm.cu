@@ -35,7 +35,7 @@ int launch_fwd(NormParams p, cudaStream_t s) {
   const int per_warp = VEC * VPT * 32;
   p.W = (p.D + per_warp - 1) / per_warp;
   const int rows = p.W == 1 ? kRowsPerCta : 1;
-  const unsigned blocks = (unsigned)((p.M + rows - 1) / rows);
+  const unsigned blocks = (unsigned)(((long long)p.M + rows - 1) / rows);
   ttt::norm_fwd_kernel<XT, RT, YT, VEC, VPT><<<blocks, 32 * p.W * rows, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }

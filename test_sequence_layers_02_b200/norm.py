@@ -15,8 +15,8 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
-                       raise_for, workspace_of, arrays)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+                       out_dtype_of, raise_for, workspace_of, arrays)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 NORM_SUM_BF16 = 1 << 18
@@ -76,15 +76,15 @@ def _forward(x, weight, residual, eps, mode, group, y, y_dtype, s, stream):
     scale = None
     with On(dev, stream, (x, weight, residual, y, s)) as st:
         if y is None:
-            y = torch.empty(shape, dtype=y_dtype, device=dev)
+            y = like(x, y_dtype)
         yp, ld_y = _rows("y", y, shape, y_dtype, dev)
         if residual is not None:
             if s is None:
-                s = torch.empty(shape, dtype=sum_dtype, device=dev)
+                s = like(residual, sum_dtype)
             sp, ld_s = _rows("s", s, shape, sum_dtype, dev)
         if mode & NORM_Y_E4M3:
             n = -(-D // 128) if group else 1
-            scale = torch.empty(shape[:-1] + (n,), dtype=_F32, device=dev)
+            scale = weight.new_empty((*shape[:-1], n))
         rc = _lib.ttt_norm_forward(xp, rp, w, M, D, eps, mode, group,
                                    _strides(D, ld_x, ld_r, ld_y, ld_s), yp, sp,
                                    None if scale is None else scale.data_ptr(), st)
@@ -148,7 +148,7 @@ def rmsnorm_backward(dy, s, weight, ds=None, *, eps: float = 1e-6,
     mode = (OUT_BF16 if dy.dtype is _BF16 else 0) | (NORM_SUM_BF16 if dtype is _BF16 else 0)
     with On(dev, stream, (dy, s, weight, ds, dx, workspace)) as st:
         if dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=dev)
+            dx = like(s, dtype)
         op, ld_o = _rows("dx", dx, shape, dtype, dev)
         workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(M, D), dev)
         dweight = torch.empty_like(weight)

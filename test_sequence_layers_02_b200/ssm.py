@@ -18,8 +18,8 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, out_dtype_of,
-                       raise_for, strides_of, workspace_of)
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+                       out_dtype_of, raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
 SSM_SOFTPLUS = 1 << 17
@@ -87,10 +87,10 @@ def selective_scan(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, *, soft
     chunks = None
     with On(dev, stream, (u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_T)) as s:
         if y is None:
-            y = torch.empty(u.shape, dtype=out_dtype, device=dev)
+            y = like(delta, out_dtype)
         yp = check("y", y, u.shape, out_dtype, dev)
         if h_T is None:
-            h_T = torch.empty((B, C, N), dtype=_F32, device=dev)
+            h_T = torch.empty((B, C, N), dtype=_F32, device=dev) if h0 is None else like(h0, _F32)
         hT = check_whole("h_T", h_T, (B, C, N), _F32, dev)
         if want_chunks:
             chunks = torch.empty((B, -(-T // CHUNK), C, N), dtype=_F32, device=dev)
@@ -132,8 +132,8 @@ def selective_scan_backward(u, delta, A, Bm, Cm, D, z, delta_bias, h_chunks, dy,
                           workspace)) as s:
         workspace, wp, wn = workspace_of(workspace, backward_workspace_bytes(B, T, C, G, N), dev)
         act = dict(dtype=u.dtype, device=dev)
-        out = dict(du=torch.empty(u.shape, **act), ddelta=torch.empty(u.shape, **act),
-                   dz=None if z is None else torch.empty(u.shape, **act),
+        out = dict(du=like(u, u.dtype), ddelta=like(u, u.dtype),
+                   dz=None if z is None else like(u, u.dtype),
                    dBm=torch.empty(bc_shape, **act), dCm=torch.empty(bc_shape, **act),
                    dA=torch.empty_like(A), dD=None if D is None else torch.empty_like(D),
                    ddelta_bias=None if delta_bias is None else torch.empty_like(delta_bias),
@@ -166,7 +166,7 @@ def selective_step(u, delta, A, Bm, Cm, D, z, delta_bias, h, *, softplus: bool =
     mode = _mode(u.dtype, out_dtype, softplus, y is None)
     with On(dev, stream, (u, delta, A, Bm, Cm, D, z, delta_bias, h, active, y)) as s:
         if y is None:
-            y = torch.empty(u.shape, dtype=out_dtype, device=dev)
+            y = like(delta, out_dtype)
         yp = check("y", y, u.shape, out_dtype, dev)
         st = strides_of(8, (u, _ROWS), (delta, _ROWS), (u.shape if z is None else z, _ROWS),
                         (Bm, _TOKENS), (Cm, _TOKENS), (y, _ROWS))

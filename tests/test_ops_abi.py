@@ -43,7 +43,8 @@ BAD_CONV = [dict(x=None), dict(weight=None), dict(y=None), dict(x=addr(0, 2)), d
 
 @pytest.mark.parametrize("over,want", [(o, INVALID) for o in BAD_CONV] +
                          [(dict(K=1), UNSUPPORTED), (dict(K=5), UNSUPPORTED),
-                          (dict(H=1 << 20, d=1 << 11, T=0), UNSUPPORTED)])
+                          (dict(H=1 << 20, d=1 << 11, T=0), UNSUPPORTED),
+                          (dict(T=(1 << 30) + 1), UNSUPPORTED)])
 def test_conv_forward(libs, over, want):
     assert libs["conv"].ttt_conv_forward(*dict(CONV, **over).values(), None) == want
 
@@ -94,8 +95,10 @@ def with_stride(i, v):
     dict(u=addr(0, 2)), dict(lengths=addr(9, 1)), dict(skip=addr(5, 2)), dict(B=-1), dict(T=-1), dict(D=0),
     dict(G=0), dict(G=5), dict(N=0), dict(mode=1), dict(y=addr(0)), dict(y=addr(6, 4)), dict(h_T=addr(8, 16)),
     dict(h_T=addr(10)), dict(chunks=addr(11)), dict(chunks=addr(3)), dict(strides=with_stride(1, -1)),
-    dict(strides=with_stride(13, 11)), dict(strides=with_stride(12, 0)))] +
-    [(dict(N=n), UNSUPPORTED) for n in (1, 4, 12, 24, 128)])
+    dict(strides=with_stride(13, 11)), dict(strides=with_stride(12, 0)),
+    dict(strides=with_stride(3, (1 << 24) + 4)))] +
+    [(dict(N=n), UNSUPPORTED) for n in (1, 4, 12, 24, 128)] +
+    [(dict(T=(1 << 30) + 1), UNSUPPORTED), (dict(D=1 << 25), UNSUPPORTED)])
 def test_ssm_forward(libs, over, want):
     assert libs["ssm"].ttt_ssm_forward(*dict(SSM, **over).values(), None) == want
 
