@@ -15,6 +15,13 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Added to the exponent of a decay. For results in (0.7, 1) ex2 is low by 0.1 to 0.45 units of 2^-24
+// on average (measured, 2^20 arguments in each of 8 ranges), which a state that lives for
+// hundreds of tokens multiplies by their number: 1.5e-6 of it after 81 tokens, measured.
+// With this the mean is within 0.2 units there, for the price of a multiply-add in the place of a
+// multiplication; an exponent of 0 still gives 1.
+constexpr float kDecayBias = 2.0e-8f;
+
 // 1 / x on the special-function unit (2^-23); 1 / inf = 0, a denormal x counts as 0.
 __device__ __forceinline__ float rcp(float x) {
   float y;

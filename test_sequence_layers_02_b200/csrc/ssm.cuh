@@ -108,6 +108,11 @@ struct LaneSum {
 __device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
+// exp(dt A), the decay of one token, for A scaled by log2 e.
+__device__ __forceinline__ float2 decay2(float2 dt, float2 A) {
+  return ex2_2(__ffma2_rn(dt, A, dup2(kDecayBias)));
+}
+
 // One channel's four states of a lane.
 struct State4 {
   float2 lo, hi;
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
           if (read) gc[j].load(&sm.C[half][t0 + j][n0]);
 #pragma unroll
           for (int i = 0; i < P / 2; ++i) {
-            ga[j].v[i] = ex2_2(__fmul2_rn(dup2(d.x), A.v[i]));
+            ga[j].v[i] = decay2(dup2(d.x), A.v[i]);
             gx[j].v[i] = __fmul2_rn(dup2(d.y), Bv.v[i]);
           }
           if (!read) sum_dt += d.x;
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) {
           s_end[i][tid] = h.v[i];
-          s_decay[i][tid] = ex2_2(__fmul2_rn(dup2(sum_dt), A.v[i]));
+          s_decay[i][tid] = decay2(dup2(sum_dt), A.v[i]);
         }
         h.zero();
         if (p.h0) h.load(p.h0 + hrow);
@@ -660,10 +665,10 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
       if (p.softplus) d = softplus(d);
       const float x = d * kLog2e, dtu = d * u[r];
       State4& s = h[r];
-      s.lo.x = fmaf(ex2(x * A.lo.x), s.lo.x, dtu * Bv[r][0]);
-      s.lo.y = fmaf(ex2(x * A.lo.y), s.lo.y, dtu * Bv[r][1]);
-      s.hi.x = fmaf(ex2(x * A.hi.x), s.hi.x, dtu * Bv[r][2]);
-      s.hi.y = fmaf(ex2(x * A.hi.y), s.hi.y, dtu * Bv[r][3]);
+      s.lo.x = fmaf(ex2(fmaf(x, A.lo.x, kDecayBias)), s.lo.x, dtu * Bv[r][0]);
+      s.lo.y = fmaf(ex2(fmaf(x, A.lo.y, kDecayBias)), s.lo.y, dtu * Bv[r][1]);
+      s.hi.x = fmaf(ex2(fmaf(x, A.hi.x, kDecayBias)), s.hi.x, dtu * Bv[r][2]);
+      s.hi.y = fmaf(ex2(fmaf(x, A.hi.y, kDecayBias)), s.hi.y, dtu * Bv[r][3]);
       float y = fmaf(Cv[r][0], s.lo.x, Cv[r][1] * s.lo.y) + fmaf(Cv[r][2], s.hi.x, Cv[r][3] * s.hi.y);
 #pragma unroll
       for (int off = L / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
       Bv.load(&sm.B[half][t][n0]);
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) {
-        at.v[i] = ex2_2(__fmul2_rn(dup2(d.x), A.v[i]));
+        at.v[i] = decay2(dup2(d.x), A.v[i]);
         qt.v[i] = __fmul2_rn(at.v[i], h.v[i]);
         h.v[i] = __ffma2_rn(dup2(d.y), Bv.v[i], qt.v[i]);
       }
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
               Cv.load(&sm.C[k & 1][t][n0]);
 #pragma unroll
               for (int i = 0; i < P / 2; ++i)
-                gr.v[i] = __fmul2_rn(ex2_2(__fmul2_rn(dt, A.v[i])), __ffma2_rn(Cv.v[i], dr, gr.v[i]));
+                gr.v[i] = __fmul2_rn(decay2(dt, A.v[i]), __ffma2_rn(Cv.v[i], dr, gr.v[i]));
               sum_dt += dt.x;
             }
           } else if (k > first) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) {
           s_start[i][tid] = gr.v[i];
-          s_decay[i][tid] = ex2_2(__fmul2_rn(dup2(sum_dt), A.v[i]));
+          s_decay[i][tid] = decay2(dup2(sum_dt), A.v[i]);
         }
         gr.zero();
         if (p.dh_T) gr.load(p.dh_T + hrow);

@@ -117,6 +117,20 @@ def test_lengths(ssm, T, lengths, N):
         assert (mine[b, n:] == 9).all() and torch.equal(mine[b, :n], y[b, :n])
 
 
+@pytest.mark.parametrize("T,n", [(40, 17), (40, 1), (700, 300)])
+def test_padding_leaves_the_state_bit_for_bit(ssm, T, n):
+    """A row of n tokens in a longer batch ends in the bits that it ends in by itself, where both go
+    through the tokens alike (one CTA: short, or without many SMs to spare)."""
+    B = 1 if T < 100 else 80
+    p = problem(B, T, 32, 16, F32, seed=n)
+    c = cuda(p)
+    full = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    y, h = ssm.selective_scan(*args(c), h0=c["h0"], lengths=full)
+    q = {k: v[:, :n].contiguous() if k in ("u", "delta", "Bm", "Cm", "z") else v for k, v in c.items()}
+    y2, h2 = ssm.selective_scan(*args(q), h0=c["h0"])
+    assert torch.equal(h, h2) and torch.equal(y[:, :n], y2)
+
+
 def test_no_tokens_and_no_rows(ssm):
     p = cuda(problem(2, 0, 6, 16, F32))
     y, h, ck = ssm.selective_scan(*args(p), h0=p["h0"], want_chunks=True)
