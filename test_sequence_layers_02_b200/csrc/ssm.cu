@@ -115,15 +115,16 @@ int launch_bwd(const SsmParams& p, cudaStream_t s) {
   return p.vec ? launch_bwd_as<N, P, InT, float, 4>(p, s) : launch_bwd_as<N, P, InT, float, 1>(p, s);
 }
 
-// Four batch rows a thread once that still leaves 16 warps for every SM.
+// Several batch rows a thread once that still leaves 16 warps for every SM.
 template <int L, typename InT, int VEC>
 int launch_step_as(const SsmParams& p, cudaStream_t s) {
+  constexpr int R = L < 4 ? L : 4;  // (of 2048 channels, 512 rows: 22 us; two rows 28 us)
   const long long blocks = ((long long)p.D * L + 255) / 256;
-  const bool four = blocks * (p.B / 2) >= 2LL * sm_count();
-  const int rows = four ? (p.B + 2 - 1) / 2 : p.B;
+  const bool several = blocks * (p.B / R) >= 2LL * sm_count();
+  const int rows = several ? (p.B + R - 1) / R : p.B;
   const dim3 grid((unsigned)blocks, rows < kMaxGridY ? rows : kMaxGridY);
-  if (four)
-    ttt::ssm_step_kernel<L, InT, VEC, 2><<<grid, 256, 0, s>>>(p);
+  if (several)
+    ttt::ssm_step_kernel<L, InT, VEC, R><<<grid, 256, 0, s>>>(p);
   else
     ttt::ssm_step_kernel<L, InT, VEC, 1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
