@@ -28,6 +28,8 @@ class Library:
         self._functions = functions
 
     def __getattr__(self, name):
+        if name not in self._functions:
+            raise AttributeError(name)
         args, res = self._functions[name]
         fn = getattr(ttt_scan.lib(), name)
         fn.argtypes, fn.restype = args, res

@@ -57,7 +57,8 @@ template <typename Kernel>
 int launch_kernel(Kernel kernel, long long blocks, int split, int B, int threads, size_t smem,
                   const SsmParams& p, cudaStream_t s) {
   if (blocks * split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
-  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // (with a split's exchange on top, static)
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return TTT_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
