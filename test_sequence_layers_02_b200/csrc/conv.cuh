@@ -9,7 +9,7 @@
 //
 // Measured, bf16, K = 4: 2 x 32768 tokens by 2048 channels into heads 105 us (537 MB: 78 % of the copy
 // bandwidth; with batches of 4 tokens 110 us); forward and backward of 8 x 4096 tokens by 768 channels, ragged,
-// 79 us, of which the backward's kernel 53 us: its windows, weights and weight sums take 128
+// 71 us, of which the backward's kernel 47 us: its windows, weights and weight sums take 128
 // registers, so 16 warps an SM, and latency is what is left; one token for 512 rows of 2048 channels 5.5 us.
 #pragma once
 
@@ -39,6 +39,7 @@ struct ConvParams {
   int vecs;             // vectors of VEC channels over all heads: H * d / VEC
   int tiles;            // runs of tokens (forward), blocks along the tokens (backward)
   int run;              // tokens per run (forward)
+  int seg;              // tokens per segment (backward)
   int silu;
   int pad_zero;         // y = 0 behind a length and in rows that are not active
 };
@@ -205,13 +206,12 @@ __global__ void __launch_bounds__(128, 5) conv_fwd_kernel(const ConvParams p) {
 }
 
 // ---- backward ----
-// A thread walks a segment of kConvSeg tokens and K - 1 beyond it: the gradient
+// A thread walks a segment of p.seg tokens and K - 1 beyond it: the gradient
 // before the activation at token t reaches dx at t - K + 1 .. t, so dx comes out
 // K - 1 tokens late from a second window. A block is 32 vectors by 8 segments; the
 // weight sums stay in registers along a segment and are added over the 8
 // segments in shared memory, one partial sum per block in global memory, added in
 // block order by reduce_parts_kernel (no atomics: the same bits on every call).
-constexpr int kConvSeg = 32;
 constexpr int kConvSegs = 8;
 
 template <typename InT, typename OutT, int VEC, int K>
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * kConvSegs, 2) conv_bwd_kernel(const ConvP
   const int cc = (on ? vec : 0) * VEC;
   const int h = cc / p.d, c = cc - h * p.d;
   const int tile = blockIdx.y;
-  const int t0 = (tile * kConvSegs + seg) * kConvSeg;
+  const int t0 = (tile * kConvSegs + seg) * p.seg;
   const long long D = (long long)p.H * p.d;
   V w[K], zero;
   load_weights<VEC, K>(p.weight, cc, w);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(32 * kConvSegs, 2) conv_bwd_kernel(const ConvP
       const InT* xp = row_ptr<InT>(p.x, p.xs, b, h, t0, c);
       const OutT* gp = row_ptr<OutT>(const_cast<const void*>(p.y), p.ys, b, h, t0, c);
       InT* dxp = row_ptr<InT>(p.dx, dxs, b, h, t0, c);
-      const int end = t0 + kConvSeg < p.T ? t0 + kConvSeg : p.T;  // dx written up to here
+      const int end = t0 + p.seg < p.T ? t0 + p.seg : p.T;  // dx written up to here
       const bool first = t0 == 0;
       // inputs t0-K+1 .. t0-1 (0 behind the length, where nothing uses them)
       V win[4], dwin[4];  // of token t at (t - t0) & 3
