@@ -53,9 +53,13 @@ struct SsmBwdShape {
   static constexpr int NBC = (BCQ + HT - 1) / HT;
   // Slots of raw inputs: from the copy to the end of the tile's epilogue, two tiles after
   // its use in staging.
-  static constexpr int RING = VEC == 1 ? 4 : sizeof(InT) == 2 ? 6 : 5;
+  static constexpr int RING = VEC > 1 && sizeof(InT) == 2 ? 6 : 5;
   static constexpr int AHEAD = RING - 3;        // tiles on their way
   static constexpr int SUMS = CW * kSsmTile * 2 * N;
+  struct Single {                               // a tile's single elements on their way
+    Pack<InT, VEC> u[IT], d[IT], z[IT], B[NBC], C[NBC];
+    Pack<OutT, VEC> g[IT];
+  };
   struct Smem {
     alignas(16) float2 dt[2][kSsmTile][CH];     // dt, dt u
     alignas(16) float dr[2][kSsmTile][CH];
@@ -138,36 +142,58 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
       Cp = static_cast<const InT*>(p.Cm) + b * p.Cm_b + g * p.Cm_g + e0 * p.Cm_t + bn;
     };
     auto slot = [&](int k) -> typename S::Smem::Slot& { return sm.ring[k % RING]; };
-    // The inputs of tile k on their way to its slot (0 behind the length); one group of
-    // copies a tile, also an empty one below the first. Single elements go through a register.
+    // The inputs of tile k on their way to its slot (0 behind the length). Packs are copied
+    // asynchronously, one group of copies a tile, also an empty one below the first; single
+    // elements wait in registers until the next call stores them, a tile later.
+    typename S::Single hold;
+    int held = -1;
     auto send = [&](int k) {
+      if constexpr (VEC == 1) {
+        if (held >= 0) {
+          typename S::Smem::Slot& r = slot(held);
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            r.u[i][tid] = hold.u[i];
+            r.d[i][tid] = hold.d[i];
+            r.z[i][tid] = hold.z[i];
+            r.g[i][tid] = hold.g[i];
+          }
+          if (bc_on) {
+#pragma unroll
+            for (int j = 0; j < NBC; ++j) {
+              r.B[j][tid] = hold.B[j];
+              r.C[j][tid] = hold.C[j];
+            }
+          }
+        }
+        held = k >= first ? k : -1;
+      }
       if (k >= first) {
         typename S::Smem::Slot& r = slot(k);
         const int left = len - k * kSsmTile;
-        auto move = [&](auto& dst, const auto* src, bool have) {
+        auto move = [&](auto& dst, auto& reg, const auto* src, bool have) {
           using T = std::remove_reference_t<decltype(dst)>;
           if constexpr (VEC > 1) {
             copy_async<sizeof(T)>(&dst, src, have);
           } else {
-            T x = {};
-            if (have) x = *reinterpret_cast<const T*>(src);
-            dst = x;
+            reg = {};
+            if (have) reg = *reinterpret_cast<const T*>(src);
           }
         };
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const bool have = it + TS * i < left;
-          move(r.u[i][tid], have ? up + TS * i * p.u_t : up, have);
-          move(r.d[i][tid], have ? dp + TS * i * p.d_t : dp, have);
-          if (p.z) move(r.z[i][tid], have ? zp + TS * i * p.z_t : zp, have);
-          move(r.g[i][tid], have ? gp + TS * i * p.y_t : gp, have);
+          move(r.u[i][tid], hold.u[i], have ? up + TS * i * p.u_t : up, have);
+          move(r.d[i][tid], hold.d[i], have ? dp + TS * i * p.d_t : dp, have);
+          if (p.z) move(r.z[i][tid], hold.z[i], have ? zp + TS * i * p.z_t : zp, have);
+          move(r.g[i][tid], hold.g[i], have ? gp + TS * i * p.y_t : gp, have);
         }
         if (bc_on) {
 #pragma unroll
           for (int j = 0; j < NBC; ++j) {
             const bool have = bt + BS * j < left;
-            move(r.B[j][tid], have ? Bp + BS * j * p.Bm_t : Bp, have);
-            move(r.C[j][tid], have ? Cp + BS * j * p.Cm_t : Cp, have);
+            move(r.B[j][tid], hold.B[j], have ? Bp + BS * j * p.Bm_t : Bp, have);
+            move(r.C[j][tid], hold.C[j], have ? Cp + BS * j * p.Cm_t : Cp, have);
           }
         }
         up -= kSsmTile * p.u_t;
