@@ -238,3 +238,18 @@ def test_refusals(norm):
     for f in lib:
         with pytest.raises(TTTScanError):
             f()
+
+
+@pytest.mark.parametrize("D,group", [(2048, 0), (2048, 128), (1000, 128), (1001, 0), (1001, 128)])
+@pytest.mark.parametrize("size", [1.0, 1e-36, 1e30])
+def test_codes_are_those_of_the_quotient(norm, D, group, size):
+    """A code is e4m3(y / scale), the quotient rounded once to fp32, for every value: also where it lies next
+    to the middle between two codes (two values in a million), and where the scale is the smallest
+    normal number."""
+    x, w, r = inputs(2048, D, BF16, BF16, seed=D)
+    a = (x.cuda(), (w * size).cuda(), r.cuda())
+    q, scale, _ = norm.rmsnorm_fp8(*a, group=group)
+    y, _ = norm.rmsnorm(*a, out_dtype=F32)     # the values before their codes, bit for bit
+    wide = scale.cpu().repeat_interleave(group or D, 1)[:, :D]
+    want = (y.cpu() / wide).to(FP8).view(torch.uint8)
+    assert torch.equal(q.cpu().view(torch.uint8), want)
