@@ -56,7 +56,7 @@ enum {
  *   state_T  [B, H, K-1, d]   out, or NULL; may be `state` itself (same strides)
  *   strides  NULL = all contiguous, or 12 element counts: between batch rows, heads and
  *            tokens (entries) of x, of y, of state and of state_T; none negative
- * Sizes: B, H, T >= 0, d >= 1, T <= 2^30 (backward: 2^22).
+ * Sizes: B, H, T >= 0, d >= 1, B <= 2^30, T <= 2^30 (backward: 2^22).
  * The extent of an output (from its first to its last element) may not meet
  * that of an input or of another output.
  */

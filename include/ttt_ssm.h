@@ -59,7 +59,7 @@ enum { TTT_SSM_CHUNK = 16 };
  *               u, of delta, of z; between rows, tokens and groups of Bm, of Cm; between rows and
  *               tokens of y; at most 2^24 between tokens. The D channels, and the N entries, are
  *               always contiguous.
- * Sizes: B, T >= 0, T <= 2^30, 1 <= D <= 2^24, G >= 1 dividing D, N in {8, 16, 32, 64}.
+ * Sizes: B, T >= 0, B <= 2^30, T <= 2^30, 1 <= D <= 2^24, G >= 1 dividing D, N in {8, 16, 32, 64}.
  * The extent of an output may not meet that of an input (except h_T = h0) or of another
  * output.
  */

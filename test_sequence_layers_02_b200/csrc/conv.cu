@@ -64,6 +64,7 @@ using ttt::abi::Strided;
 constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_CONV_SILU | TTT_CONV_PAD_ZERO;
 constexpr int kMaxGridY = 65535;
 constexpr int kMaxT = 1 << 30;  // token numbers and a run beyond them fit an int
+constexpr int kMaxB = 1 << 30;  // row numbers and a grid's height beyond them fit an int
 
 enum Which { kForward, kBackward, kStep };
 
@@ -137,7 +138,7 @@ int check_sizes(int B, int H, int T, int d, int K, unsigned mode) {
   if (mode & ~kKnownModes) return TTT_ERR_INVALID_ARG;
   if (B < 0 || H < 0 || T < 0 || d < 1 || K < 1) return TTT_ERR_INVALID_ARG;
   if (K < 2 || K > 4) return TTT_ERR_UNSUPPORTED;
-  if ((long long)H * d * K > 0x7fffffffLL || T > kMaxT) return TTT_ERR_UNSUPPORTED;
+  if ((long long)H * d * K > 0x7fffffffLL || T > kMaxT || B > kMaxB) return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 

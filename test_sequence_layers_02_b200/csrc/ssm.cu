@@ -20,13 +20,14 @@ using ttt::abi::Strided;
 constexpr unsigned kKnownModes = TTT_IN_BF16 | TTT_OUT_BF16 | TTT_SSM_SOFTPLUS | TTT_SSM_PAD_ZERO;
 constexpr int kMaxGridY = 65535;
 constexpr int kMaxT = 1 << 30;  // token numbers and a tile beyond them fit an int
+constexpr int kMaxB = 1 << 30;  // row numbers and a grid's height beyond them fit an int
 constexpr long long kMaxTokenStride = 1 << 24;  // 16 tokens of 4 bytes and a row of channels: 32 bits
 
 int check_sizes(int B, int T, int D, int G, int N, unsigned mode) {
   if (mode & ~kKnownModes) return TTT_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || D < 1 || G < 1 || N < 1 || D % G != 0) return TTT_ERR_INVALID_ARG;
   if (N != 8 && N != 16 && N != 32 && N != 64) return TTT_ERR_UNSUPPORTED;
-  if (T > kMaxT || D > kMaxTokenStride || (long long)G * N > kMaxTokenStride || (long long)D * N > 0x7fffffffLL)
+  if (T > kMaxT || B > kMaxB || D > kMaxTokenStride || (long long)G * N > kMaxTokenStride || (long long)D * N > 0x7fffffffLL)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }

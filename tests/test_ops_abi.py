@@ -168,3 +168,28 @@ def test_workspace_sizes(libs):
     assert ssm.ttt_ssm_backward_workspace_bytes(1, 100000, 64, 1, 16) > 100000 * 32 * 4
     assert norm.ttt_norm_backward_workspace_bytes(0, 64) == 0
     assert norm.ttt_norm_backward_workspace_bytes(3, 64) == 3 * 64 * 4
+
+
+@pytest.mark.parametrize("rows,want", [((1 << 30) + 1, UNSUPPORTED), ((1 << 31) - 1, UNSUPPORTED)])
+def test_rows_beyond_what_the_kernels_count(libs, rows, want):
+    """Row numbers and the rows of a grid beyond them fit an int."""
+    far = lambda i: (i + 1) << 56  # noqa: E731  (room for tensors of that many rows)
+    one = dict(B=rows, H=1, T=1, d=1)
+    a = dict(CONV, **one, x=far(0), state=None, lengths=None, weight=far(1), bias=None, y=far(2), state_T=None)
+    assert libs["conv"].ttt_conv_forward(*a.values(), None) == want
+    a = dict(CONV_BWD, **one, x=far(0), weight=far(1), bias=None, state=None, dy=far(2), dstate_T=None, dx=far(3),
+             dweight=far(4), dbias=None, dstate=None, ws=far(5), ws_bytes=1 << 50)
+    assert libs["conv"].ttt_conv_backward(*a.values(), None) == want
+    a = dict(x=far(0), weight=far(1), bias=None, state=far(2), active=None, B=rows, H=1, d=1, K=4, mode=0,
+             strides=None, y=far(3))
+    assert libs["conv"].ttt_conv_step(*a.values(), None) == want
+    names = ("u", "delta", "A", "Bm", "Cm", "skip", "z", "bias", "h0", "lengths")
+    a = dict(SSM, **{k: far(i) for i, k in enumerate(names)}, B=rows, T=1, D=1, G=1, N=8, y=far(10), h_T=far(11),
+             chunks=None)
+    assert libs["ssm"].ttt_ssm_forward(*a.values(), None) == want
+    keys = [k for k, v in SSM_BWD.items() if v is not None and k not in ("B", "T", "D", "G", "N", "mode", "ws_bytes")]
+    a = dict(SSM_BWD, **{k: far(i) for i, k in enumerate(keys)}, B=rows, T=1, D=1, G=1, N=8, ws_bytes=1 << 60)
+    assert libs["ssm"].ttt_ssm_backward(*a.values(), None) == want
+    a = dict(u=far(0), delta=far(1), A=far(2), Bm=far(3), Cm=far(4), skip=None, z=None, bias=None, h=far(5),
+             active=None, B=rows, D=1, G=1, N=8, mode=0, strides=None, y=far(6))
+    assert libs["ssm"].ttt_ssm_step(*a.values(), None) == want
