@@ -257,7 +257,7 @@ int ttt_conv_backward(const void* x, const float* weight, const float* bias, con
   p.seg = bwd_seg(B, H, T, d);
   p.tiles = bwd_tiles(B, H, T, d);
   if (p.tiles > kMaxGridY) return TTT_ERR_UNSUPPORTED;
-  if ((long long)B * p.tiles > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
+  if ((long long)B * p.tiles > kMaxB) return TTT_ERR_UNSUPPORTED;  // rows of partial sums
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const long long D = (long long)H * d;
   if (!rows) {

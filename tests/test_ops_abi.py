@@ -193,3 +193,14 @@ def test_rows_beyond_what_the_kernels_count(libs, rows, want):
     a = dict(u=far(0), delta=far(1), A=far(2), Bm=far(3), Cm=far(4), skip=None, z=None, bias=None, h=far(5),
              active=None, B=rows, D=1, G=1, N=8, mode=0, strides=None, y=far(6))
     assert libs["ssm"].ttt_ssm_step(*a.values(), None) == want
+
+
+def test_partial_sums_beyond_what_their_reduction_counts(libs):
+    """Rows times blocks along the tokens: the reduction's row number and a step beyond it fit an int."""
+    far = lambda i: (i + 1) << 56  # noqa: E731
+    for B, T in (((1 << 30) - 1, 100), (1 << 24, 40000)):
+        a = dict(CONV_BWD, B=B, H=1, T=T, d=1, K=2, x=far(0), weight=far(1), bias=None, state=None, dy=far(2),
+                 dstate_T=None, dx=far(3), dweight=far(4), dbias=None, dstate=None, ws=far(5), ws_bytes=1 << 50)
+        parts = libs["conv"].ttt_conv_backward_workspace_bytes(B, 1, T, 1, 2) // 12
+        assert 1 << 30 < parts < 1 << 31
+        assert libs["conv"].ttt_conv_backward(*a.values(), None) == UNSUPPORTED
