@@ -198,7 +198,7 @@ def test_rows_beyond_what_the_kernels_count(libs, rows, want):
 def test_partial_sums_beyond_what_their_reduction_counts(libs):
     """Rows times blocks along the tokens: the reduction's row number and a step beyond it fit an int."""
     far = lambda i: (i + 1) << 56  # noqa: E731
-    for B, T in (((1 << 30) - 1, 100), (1 << 24, 40000)):
+    for B, T in (((1 << 30) - 1, 600), (1 << 24, 40000)):
         a = dict(CONV_BWD, B=B, H=1, T=T, d=1, K=2, x=far(0), weight=far(1), bias=None, state=None, dy=far(2),
                  dstate_T=None, dx=far(3), dweight=far(4), dbias=None, dstate=None, ws=far(5), ws_bytes=1 << 50)
         parts = libs["conv"].ttt_conv_backward_workspace_bytes(B, 1, T, 1, 2) // 12
