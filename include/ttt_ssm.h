@@ -43,8 +43,9 @@ enum { TTT_SSM_CHUNK = 16 };
  * where noted:
  *   u, delta, z [B, T, D]   fp32, or bf16 with TTT_IN_BF16; z NULL = no output gate
  *   Bm, Cm      [B, T, G, N] same type
- *   A           [D, N]      fp32, contiguous, 16-byte aligned; finite, and A dt <= 0 for a state that
- *                           decays (nothing is clipped: a growing one may leave fp32's range)
+ *   A           [D, N]      fp32, contiguous, 16-byte aligned; finite (beyond 2.35e38 it counts as
+ *                           that), and A dt <= 0 for a state that decays (a growing one may leave
+ *                           fp32's range)
  *   skip, delta_bias [D]    fp32; NULL = 0
  *   h0          [B, D, N]   fp32, contiguous, 16-byte aligned; NULL = zeros
  *   lengths     [B]         int32 tokens of each row, clipped to [0, T]; NULL = T. Tokens at or

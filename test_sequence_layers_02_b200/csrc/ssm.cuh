@@ -108,6 +108,17 @@ struct LaneSum {
 __device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
+// A log2 e, kept finite: with an infinite one a step of 0 would decay by exp(0 inf), which is no number. So an
+// A beyond 2.35e38 counts as that (its decay over any step above 1e-36 is 0 either way).
+__device__ __forceinline__ float scaled_rate(float A) {
+  constexpr float kMax = 3.402823466e38f;
+  const float x = A * kLog2e;
+  return x < -kMax ? -kMax : x > kMax ? kMax : x;
+}
+__device__ __forceinline__ float2 scaled_rate2(float2 A) {
+  return make_float2(scaled_rate(A.x), scaled_rate(A.y));
+}
+
 // exp(dt A), the decay of one token, for A scaled by log2 e.
 __device__ __forceinline__ float2 decay2(float2 dt, float2 A) {
   return ex2_2(__ffma2_rn(dt, A, dup2(kDecayBias)));
@@ -242,7 +253,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
   States<P> A;
   A.load(p.A + par);
 #pragma unroll
-  for (int i = 0; i < P / 2; ++i) A.v[i] = __fmul2_rn(A.v[i], dup2(kLog2e));
+  for (int i = 0; i < P / 2; ++i) A.v[i] = scaled_rate2(A.v[i]);
 
   // the others: tokens it + TS i of channels ic .. ic + VEC - 1
   const int ic = tid % QUADS * VEC, it = tid / QUADS;
@@ -635,8 +646,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
   const int g = cc / p.per_group;
   const size_t par = (size_t)cc * N + n0;
   State4 A = load_state(p.A + par);
-  A.lo = __fmul2_rn(A.lo, dup2(kLog2e));
-  A.hi = __fmul2_rn(A.hi, dup2(kLog2e));
+  A.lo = scaled_rate2(A.lo);
+  A.hi = scaled_rate2(A.hi);
   const float bias = p.delta_bias ? p.delta_bias[cc] : 0.f;
   const float skip = p.skip ? p.skip[cc] : 0.f;
   const int mine = Sum::first(lane % L);  // the row of this lane's scalars

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
   States<P> A;
   A.load(p.A + par);
 #pragma unroll
-  for (int i = 0; i < P / 2; ++i) A.v[i] = __fmul2_rn(A.v[i], dup2(kLog2e));
+  for (int i = 0; i < P / 2; ++i) A.v[i] = scaled_rate2(A.v[i]);
 
   // the others: tokens it + TS i of channels ic .. ic + VEC - 1
   const int ic = tid % QUADS * VEC, it = tid / QUADS;

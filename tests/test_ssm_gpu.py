@@ -412,3 +412,36 @@ def test_refusals(ssm):
     _, _, ck = ssm.selective_scan(*a, want_chunks=True)
     with pytest.raises(TTTScanError):     # too small a workspace
         ssm.selective_scan_backward(*a, ck, p["u"].clone(), workspace=torch.empty(4, device="cuda"))
+
+
+LOWEST = torch.finfo(F32).min
+
+
+@pytest.mark.parametrize("N", [8, 16, 64])
+@pytest.mark.parametrize("T,lengths", [(20, None), (20, [20, 5, 0]), (16, None), (300, [300, 129, 7])])
+def test_states_that_are_switched_off(ssm, T, lengths, N):
+    """The lowest fp32 value in A (and one that only a factor of log2 e takes out of range): exp(dt A) is 0 at a
+    step and 1 where there is none, behind a length, in a tile's last tokens or in an empty span."""
+    p = problem(3, T, 12, N, F32, seed=T + N, lengths=lengths)
+    p["A"][:, 3] = LOWEST
+    p["A"][5] = -2.5e38
+    y, h, _ = check_forward(ssm, p)
+    assert torch.isfinite(y).all() and torch.isfinite(h).all()
+    check_backward(ssm, p)
+
+
+@pytest.mark.parametrize("N", [8, 16, 64])
+def test_step_of_no_length_with_a_state_switched_off(ssm, N):
+    """A step size of 0 (softplus of a large negative number) leaves every state as it is."""
+    p = problem(3, 1, 12, N, F32, seed=N)
+    p["A"][:, 3] = LOWEST
+    p["delta"][1] = -300.0
+    one = cuda({k: v[:, 0] if k in ("u", "delta", "Bm", "Cm", "z") else v for k, v in p.items()})
+    h = one["h0"].clone()
+    y = ssm.selective_step(*args(one), h)
+    q = clean(p)
+    ry, rh = ref.scan(*args(q), q["h0"], None)
+    assert ref.rrms(y, ry[:, 0]) <= ref.tol(F32, 1) and ref.rrms(h, rh) <= ref.tol(F32, 1)
+    assert torch.equal(h[1], one["h0"][1])
+    y, h = ssm.selective_scan(*args(cuda(p)), h0=one["h0"])
+    assert ref.rrms(y, ry) <= ref.tol(F32, 1) and ref.rrms(h, rh) <= ref.tol(F32, 1)
