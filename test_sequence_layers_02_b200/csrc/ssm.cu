@@ -59,7 +59,7 @@ int launch_kernel(Kernel kernel, long long blocks, int split, int B, int threads
                   const SsmParams& p, cudaStream_t s) {
   if (blocks * split > 0x7fffffffLL) return TTT_ERR_UNSUPPORTED;
   // (with a split's exchange on top, static)
-  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 24 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return TTT_ERR_CUDA;
   cudaLaunchConfig_t cfg{};

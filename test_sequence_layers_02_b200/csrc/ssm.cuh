@@ -124,6 +124,16 @@ __device__ __forceinline__ float2 decay2(float2 dt, float2 A) {
   return ex2_2(__ffma2_rn(dt, A, dup2(kDecayBias)));
 }
 
+// d h + a, what is left of a state h behind a span with the decay d and the span's own, where d alone may leave
+// fp32's range: a state that grows need not, nothing stays nothing, and a small one is multiplied in
+// steps. x is the exponent of d, for ex2.
+__device__ __forceinline__ float carry_span(float d, float x, float h, float a) {
+  if (d != __int_as_float(0x7f800000) || h != h) return fmaf(d, h, a);
+  if (h == 0.f) return a;
+  const float q = ex2(0.25f * x);  // h >= 2^-149: beyond 4 * 128 it is out of range either way
+  return fmaf(q * (q * (q * h)), q, a);
+}
+
 // One channel's four states of a lane.
 struct State4 {
   float2 lo, hi;
@@ -156,6 +166,22 @@ struct States {
         v[2 * i] = make_float2(x.x, x.y);
         v[2 * i + 1] = make_float2(x.z, x.w);
       }
+    }
+  }
+  __device__ __forceinline__ bool finite() const {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) s = fmaf(0.f, v[i].x, fmaf(0.f, v[i].y, s));
+    return s == 0.f;
+  }
+  // carry_span for all states: a span's decays and own states by index, its sum of step sizes
+  template <typename Decay, typename Own>
+  __device__ __forceinline__ void carry(Decay decay, Own own, float sum_dt, const States& A) {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const float2 d = decay(i), a = own(i);
+      v[i] = make_float2(carry_span(d.x, sum_dt * A.v[i].x, v[i].x, a.x),
+                         carry_span(d.y, sum_dt * A.v[i].y, v[i].y, a.y));
     }
   }
   __device__ __forceinline__ void store(float* p) const {
@@ -233,6 +259,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
   extern __shared__ __align__(16) unsigned char smem_raw[];
   typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(smem_raw);
   __shared__ float2 s_end[SPLIT ? P / 2 : 1][SPLIT ? RT : 1], s_decay[SPLIT ? P / 2 : 1][SPLIT ? RT : 1];
+  __shared__ float s_sum[SPLIT ? RT : 1];
 
   enum { kRecur, kStage, kWrite };
   const int role = threadIdx.x < RT ? kRecur : threadIdx.x < RT + HT ? kStage : kWrite;
@@ -570,6 +597,7 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
         }
       }
       if (role == kRecur) {
+        s_sum[tid] = sum_dt;
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) {
           s_end[i][tid] = h.v[i];
@@ -585,6 +613,14 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
           for (int i = 0; i < P / 2; ++i)
             h.v[i] = __ffma2_rn(*cluster.map_shared_rank(&s_decay[i][tid], r), h.v[i],
                                 *cluster.map_shared_rank(&s_end[i][tid], r));
+        }
+        if (!h.finite()) {  // once more, with care
+          h.zero();
+          if (p.h0) h.load(p.h0 + hrow);
+          for (int r = 0; r < rank; ++r)
+            h.carry([&](int i) { return *cluster.map_shared_rank(&s_decay[i][tid], r); },
+                    [&](int i) { return *cluster.map_shared_rank(&s_end[i][tid], r); },
+                    *cluster.map_shared_rank(&s_sum[tid], r), A);
         }
       }
       cluster.sync();  // nobody writes or leaves while its shared memory is read

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
   extern __shared__ __align__(16) unsigned char smem_raw[];
   typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(smem_raw);
   __shared__ float2 s_start[SPLIT ? P / 2 : 1][SPLIT ? RT : 1], s_decay[SPLIT ? P / 2 : 1][SPLIT ? RT : 1];
+  __shared__ float s_sum[SPLIT ? RT : 1];
 
   const bool recur = threadIdx.x < RT;
   const int tid = recur ? threadIdx.x : threadIdx.x - RT;  // within the role
@@ -387,6 +388,7 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
         if constexpr (VEC > 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       if (recur) {
+        s_sum[tid] = sum_dt;
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) {
           s_start[i][tid] = gr.v[i];
@@ -402,6 +404,14 @@ __global__ void __launch_bounds__(SsmBwdShape<N, P, InT, OutT, VEC>::NT, N <= 16
           for (int i = 0; i < P / 2; ++i)
             gr.v[i] = __ffma2_rn(*cluster.map_shared_rank(&s_decay[i][tid], r), gr.v[i],
                                  *cluster.map_shared_rank(&s_start[i][tid], r));
+        }
+        if (!gr.finite()) {  // once more, with care
+          gr.zero();
+          if (p.dh_T) gr.load(p.dh_T + hrow);
+          for (int r = p.split - 1; r > rank; --r)
+            gr.carry([&](int i) { return *cluster.map_shared_rank(&s_decay[i][tid], r); },
+                     [&](int i) { return *cluster.map_shared_rank(&s_start[i][tid], r); },
+                     *cluster.map_shared_rank(&s_sum[tid], r), A);
         }
       }
       cluster.sync();  // nobody writes or leaves while its shared memory is read

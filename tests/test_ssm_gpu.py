@@ -445,3 +445,39 @@ def test_step_of_no_length_with_a_state_switched_off(ssm, N):
     assert torch.equal(h[1], one["h0"][1])
     y, h = ssm.selective_scan(*args(cuda(p)), h0=one["h0"])
     assert ref.rrms(y, ry) <= ref.tol(F32, 1) and ref.rrms(h, rh) <= ref.tol(F32, 1)
+
+
+@pytest.mark.parametrize("N", [8, 16, 32])
+def test_growth_beyond_range_over_a_span_of_nothing(ssm, N):
+    """States that would grow by more than fp32 holds over a span of a split prompt, but have nothing to
+    grow from: they stay 0, as in a prompt that is not split. Likewise a gradient of 0 on its way back."""
+    B, T, C = 1, 400, 8
+    p = problem(B, T, C, N, F32, seed=N, h0=False, bias=False)
+    p["A"], p["delta"] = torch.full((C, N), 2.0), torch.ones(B, T, C)
+    p["u"][:, :T - 6] = 0                  # the states start in the last span, and grow by e^12
+    y, h, ck = check_forward(ssm, p, softplus=False)
+    assert not h.isnan().any() and not y[:, :T - 6].any()
+    # and back: gradients that start in the first span, below states of 0
+    p["u"].zero_()
+    dy = torch.zeros(B, T, C)
+    dy[:, :3] = torch.randn(B, 3, C, generator=torch.Generator().manual_seed(3))
+    c, q = cuda(p), clean(p)
+    _, _, ck = ssm.selective_scan(*args(c), softplus=False, want_chunks=True)
+    r = ssm.selective_scan_backward(*args(c), ck, dy.cuda(), softplus=False)
+    leaves = [None if q[k] is None else q[k].requires_grad_() for k in NAMES]
+    want = ref.gradients(ref.scan(*leaves, None, None, False)[:1], (ref.up(dy),), leaves)
+    for k, w in zip(GRADS, want):
+        if w is not None:
+            assert ref.rrms(r[k], w) <= ref.tol(F32, T, C * T), k
+
+
+def test_growth_beyond_range_of_a_small_state(ssm):
+    """1e-20 e^100 = 2.7e23 is a number of fp32, e^100 is not; the second half of the tokens leave it as it is."""
+    B, T, C, N = 1, 160, 4, 16
+    p = problem(B, T, C, N, F32, seed=1, bias=False)
+    p["u"].zero_()
+    p["h0"] = torch.full((B, C, N), 1e-20)
+    p["A"] = torch.full((C, N), 100 / 80)
+    p["delta"] = torch.cat((torch.ones(B, 80, C), torch.zeros(B, 80, C)), 1)
+    y, h, _ = check_forward(ssm, p, softplus=False)
+    assert torch.isfinite(h).all()
