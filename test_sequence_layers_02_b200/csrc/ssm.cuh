@@ -111,9 +111,10 @@ __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x),
 // A log2 e, kept finite: with an infinite one a step of 0 would decay by exp(0 inf), which is no number. So an
 // A beyond 2.35e38 counts as that (its decay over any step above 1e-36 is 0 either way).
 __device__ __forceinline__ float scaled_rate(float A) {
-  constexpr float kMax = 3.402823466e38f;
-  const float x = A * kLog2e;
-  return x < -kMax ? -kMax : x > kMax ? kMax : x;
+  float x = A * kLog2e;  // (and NaN stays NaN)
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(3.402823466e38f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-3.402823466e38f));
+  return x;
 }
 __device__ __forceinline__ float2 scaled_rate2(float2 A) {
   return make_float2(scaled_rate(A.x), scaled_rate(A.y));
