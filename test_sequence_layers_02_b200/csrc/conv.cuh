@@ -279,10 +279,12 @@ __global__ void __launch_bounds__(32 * kConvSegs, 2) conv_bwd_kernel(const ConvP
         }
         if (!inner && t >= len) g = zero;
         dwin[j & 3] = g;
-        if (!inner && t >= end) g = zero;
-        db.add(g);
+        // (not as a product with 0: the window may hold an infinite input)
+        if (inner || (t < len && t < end)) {
+          db.add(g);
 #pragma unroll
-        for (int q = 0; q < K; ++q) dw[q].fma(g, win[(j - (K - 1) + q) & 3]);
+          for (int q = 0; q < K; ++q) dw[q].fma(g, win[(j - (K - 1) + q) & 3]);
+        }
         const int e = t - (K - 1);  // the input whose gradient is complete now
         if (!inner && (e >= end || (e < t0 && !(first && e < 0)))) return;
         V out = w[K - 1];

@@ -306,3 +306,27 @@ def test_refusals(conv):
     for f in lib:
         with pytest.raises(conv.raise_for.__globals__["TTTScanError"]):
             f()
+
+
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("T,lengths", [(24, None), (83, [83, 40, 9])])
+def test_an_infinite_input_stays_in_its_own_products(conv, T, lengths, K):
+    """The last token reaches the weight gradient of its own tap alone: an infinity there leaves the others."""
+    B, D = 3, 12
+    p = problem(B, T, D, K, F32, seed=K, lengths=lengths)
+    n = lengths or [T] * B
+    p["x"][0, n[0] - 1, 5] = float("inf")
+    dy = torch.randn(B, T, D, generator=torch.Generator().manual_seed(2)) ** 2 + 0.5
+    c = cuda(p)
+    r = conv.causal_conv_backward(c["x"], c["weight"], c["bias"], dy.cuda(), silu=False, state=c["state"],
+                                  lengths=c["lengths"])
+    want = torch.zeros(D, K, dtype=torch.float64)
+    for b in range(B):
+        ext = torch.cat((ref.up(p["state"])[b], ref.up(p["x"])[b, :n[b]]))
+        for j in range(K):
+            want[:, j] += (ref.up(dy)[b, :n[b]] * ext[j:j + n[b]]).sum(0)
+    assert want[5, K - 1] == float("inf") and torch.isfinite(want[5, :K - 1]).all()
+    assert r["dweight"][5, K - 1] == float("inf")
+    got, want = r["dweight"].clone(), want.clone()
+    got[5, K - 1] = want[5, K - 1] = 0
+    assert ref.rrms(got, want) <= bound(F32, K) * (1 + (B * T) ** 0.5)
