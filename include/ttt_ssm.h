@@ -58,8 +58,8 @@ enum { TTT_SSM_CHUNK = 16 };
  *               token, for the backward (slots of chunks past a row's length are left as they were)
  *   strides     NULL = all contiguous, or 14 element counts, none negative: between rows and tokens of
  *               u, of delta, of z; between rows, tokens and groups of Bm, of Cm; between rows and
- *               tokens of y; at most 2^24 between tokens. The D channels, and the N entries, are
- *               always contiguous.
+ *               tokens of y; at most 2^24 between tokens (any with T <= 1). The D channels, and
+ *               the N entries, are always contiguous.
  * Sizes: B, T >= 0, B <= 2^30, T <= 2^30, 1 <= D <= 2^24, G >= 1 dividing D, N in {8, 16, 32, 64}.
  * The extent of an output may not meet that of an input (except h_T = h0) or of another
  * output.

@@ -161,8 +161,8 @@ int dispatch(const SsmParams& p, int N, unsigned mode, cudaStream_t s) {
   return (mode & TTT_IN_BF16) ? dispatch_n<W, __nv_bfloat16>(p, N, s) : dispatch_n<W, float>(p, N, s);
 }
 
-// Strides of a prompt's tensors into p (null: contiguous). False: a token stride
-// that is negative or too long for the kernels' arithmetic within a tile.
+// Strides of a prompt's tensors into p (null: contiguous). False: a token stride that is
+// negative or too long for the kernels' arithmetic within a tile, where there are two tokens.
 bool set_strides(SsmParams& p, int T, int D, int G, int N, const long long* s) {
   const long long tok = (long long)T * D, vec = (long long)T * G * N, gn = (long long)G * N;
   const long long whole[14] = {tok, D, tok, D, tok, D, vec, gn, N, vec, gn, N, tok, D};
@@ -172,6 +172,7 @@ bool set_strides(SsmParams& p, int T, int D, int G, int N, const long long* s) {
   const long long t[6] = {s[1], s[3], s[5], s[7], s[10], s[13]};
   int* to[6] = {&p.u_t, &p.d_t, &p.z_t, &p.Bm_t, &p.Cm_t, &p.y_t};
   for (int i = 0; i < 6; ++i) {
+    if (T <= 1) { *to[i] = 0; continue; }  // (no distance to go)
     if (t[i] < 0 || t[i] > kMaxTokenStride) return false;
     *to[i] = (int)t[i];
   }

@@ -481,3 +481,22 @@ def test_growth_beyond_range_of_a_small_state(ssm):
     p["delta"] = torch.cat((torch.ones(B, 80, C), torch.zeros(B, 80, C)), 1)
     y, h, _ = check_forward(ssm, p, softplus=False)
     assert torch.isfinite(h).all()
+
+
+def test_one_token_of_a_token_major_batch(ssm):
+    """T = 1: the distance between tokens does not matter, however long."""
+    B, C, N = 3, 16, 16
+    p = problem(B, 1, C, N, F32, seed=2)
+    c = cuda(p)
+    y, h, ck = ssm.selective_scan(*args(c), h0=c["h0"], want_chunks=True)
+    dy = torch.randn(B, 1, C, device="cuda")
+    r = ssm.selective_scan_backward(*args(c), ck, dy, h)
+    wide = torch.zeros(B, 3 * C, device="cuda")
+    far = dict(c)
+    for i, k in enumerate(("u", "delta", "z")):   # slices of a projection [1, B, 3 C] of a larger batch
+        wide[:, i * C:(i + 1) * C] = c[k][:, 0]
+        far[k] = torch.as_strided(wide, (B, 1, C), (3 * C, 1 << 25, 1), i * C)
+    assert not far["u"].is_contiguous()
+    y2, h2, ck2 = ssm.selective_scan(*args(far), h0=c["h0"], want_chunks=True)
+    r2 = ssm.selective_scan_backward(*args(far), ck2, dy, h)
+    assert torch.equal(y, y2) and torch.equal(h, h2) and all(torch.equal(r[k], r2[k]) for k in r)
