@@ -7,7 +7,7 @@
 // such rows share a CTA. Rows whose pointers or strides are off 16 bytes, or
 // with D not a multiple of 8, take the same kernel with single columns.
 //
-// Measured, bf16: 65536 rows of 2048 in 8 bits, a scale for each 128 columns, 157 us (944 MB: 91 % of the copy
+// Measured, bf16: 65536 rows of 2048 in 8 bits, a scale for each 128 columns, 150 us (944 MB: 96 % of the copy
 // bandwidth); 32768 rows of 1536 forward 58 us (403 MB: 105 %, part of it still in L2) and backward
 // 72 us and 8 us for the sum of the weight gradients' parts; 64 rows of 2048 in 8 bits 3.8 us.
 #pragma once
@@ -82,8 +82,22 @@ __device__ __forceinline__ int norm_column(int warp, int lane, int v) {
   return ((warp * VPT + v) * 32 + lane) * VEC;
 }
 
+// The most threads a forward launch takes: rows of up to 16384 single columns in 32 warps; of 8
+// columns a lane in 16 warps of 1024 columns or 8 of 512.
+template <int VEC, int VPT>
+constexpr int norm_fwd_threads() {
+  return VEC == 1 ? 1024 : VPT == 4 ? 512 : 256;
+}
+// Of those that an SM has to hold (0: as it comes). The 32 columns a lane of VPT = 4 otherwise take a few
+// registers more than 64: 65536 rows of 2048 in bf16 183 us, so 157; in 8 bits 158, so 150.
+template <int VEC, int VPT>
+constexpr int norm_fwd_ctas() {
+  return VEC == 1 ? 1 : VPT == 4 ? 2 : 0;
+}
+
 template <typename XT, typename RT, typename YT, int VEC, int VPT>
-__global__ void norm_fwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VEC, VPT>())
+    norm_fwd_kernel(const NormParams p) {
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31;
   const int warp = (threadIdx.x >> 5) % p.W, sub = (threadIdx.x >> 5) / p.W;

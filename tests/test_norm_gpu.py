@@ -253,3 +253,37 @@ def test_codes_are_those_of_the_quotient(norm, D, group, size):
     wide = scale.cpu().repeat_interleave(group or D, 1)[:, :D]
     want = (y.cpu() / wide).to(FP8).view(torch.uint8)
     assert torch.equal(q.cpu().view(torch.uint8), want)
+
+
+# Rows off 8 columns that take from 3 to 32 warps, a column a lane; beyond 8192 a CTA of 1024 threads.
+ODD = [1023, 1535, 4099, 8191, 8193, 12289, 16383]
+
+
+@pytest.mark.parametrize("D", ODD)
+@pytest.mark.parametrize("dtype,res,out", [(F32, F32, F32), (BF16, BF16, BF16), (BF16, F32, BF16), (F32, BF16, BF16)])
+def test_long_rows_off_8_columns(norm, D, dtype, res, out):
+    x, w, r = inputs(9, D, dtype, res, seed=D)
+    y, s = norm.rmsnorm(x.cuda(), w.cuda(), r.cuda(), out_dtype=out, eps=1e-5)
+    ry, _ = ref.norm(ref.up(x), ref.up(w), ref.up(r), 1e-5)
+    assert y.dtype == out and ref.rrms(y, ry) <= bound(out, D)
+    assert torch.equal(s.cpu(), (x.float() + r.float()).to(res))
+    for group in (0, 128):
+        q, scale, _ = norm.rmsnorm_fp8(x.cuda(), w.cuda(), r.cuda(), group=group, eps=1e-5)
+        parts = [ry[:, i:i + (group or D)] for i in range(0, D, group or D)]
+        assert ref.rrms(scale, torch.stack([p.abs().amax(1) for p in parts], 1) / 448) <= bound(F32, D)
+        check_codes(q, scale, ry, group)
+
+
+@pytest.mark.parametrize("D", ODD)
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_backward_of_long_rows_off_8_columns(norm, D, dtype, out):
+    M = 11
+    x, w, _ = inputs(M, D, dtype, None, seed=D + M)
+    g = torch.Generator().manual_seed(1)
+    dy, ds = torch.randn(M, D, generator=g).to(out), torch.randn(M, D, generator=g).to(dtype)
+    leaves = [ref.up(x).requires_grad_(), ref.up(w).requires_grad_()]
+    y, s = ref.norm(*leaves, None, 1e-3)
+    want = ref.gradients((y, s), (ref.up(dy), ref.up(ds)), leaves)
+    r = norm.rmsnorm_backward(dy.cuda(), x.cuda(), w.cuda(), ds.cuda(), eps=1e-3)
+    assert ref.rrms(r["dx"], want[0]) <= bound(dtype, D) * 4
+    assert ref.rrms(r["dweight"], want[1]) <= bound(F32, D) * (1 + M ** 0.5)
