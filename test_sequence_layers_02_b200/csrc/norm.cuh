@@ -49,9 +49,16 @@ struct NormBwdParams {
 
 struct E4M3 {};  // 8-bit output
 
+// The larger number; NaN where one of them is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  for (int off = 16; off > 0; off >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, off));
   return x;
 }
 
@@ -174,18 +181,18 @@ __global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VE
     for (int v = 0; v < VPT; ++v) {
       amax[v] = 0.f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) amax[v] = fmaxf(amax[v], fabsf(s[v][i]));
+      for (int i = 0; i < VEC; ++i) amax[v] = max_nan(amax[v], fabsf(s[v][i]));
     }
     if (!p.group128) {
       float m = 0.f;
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) m = fmaxf(m, amax[v]);
+      for (int v = 0; v < VPT; ++v) m = max_nan(m, amax[v]);
       m = warp_max(m);
       if (p.W > 1) {
         if (lane == 0) red[1][warp] = m;
         __syncthreads();
         m = 0.f;
-        for (int w = 0; w < p.W; ++w) m = fmaxf(m, red[1][w]);
+        for (int w = 0; w < p.W; ++w) m = max_nan(m, red[1][w]);
       }
 #pragma unroll
       for (int v = 0; v < VPT; ++v) amax[v] = m;
@@ -194,12 +201,12 @@ __global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VE
       for (int v = 0; v < VPT; ++v)
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1)
-          amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], off));
+          amax[v] = max_nan(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], off));
     } else {
       static_assert(VEC == 8 || VPT % 4 == 0, "whole groups of 128 columns");
 #pragma unroll
       for (int v = 0; v < VPT; v += 4) {
-        const float m = warp_max(fmaxf(fmaxf(amax[v], amax[v + 1]), fmaxf(amax[v + 2], amax[v + 3])));
+        const float m = warp_max(max_nan(max_nan(amax[v], amax[v + 1]), max_nan(amax[v + 2], amax[v + 3])));
         amax[v] = amax[v + 1] = amax[v + 2] = amax[v + 3] = m;
       }
     }
@@ -209,8 +216,8 @@ __global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VE
     for (int v = 0; v < VPT; ++v) {
       const int c = norm_column<VEC, VPT>(warp, lane, v);
       if (c >= p.D) continue;
-      // at least the smallest normal number: a row of zeros stays dividable
-      const float scale = fmaxf(amax[v] / 448.f, 1.17549435e-38f);
+      // At least the smallest normal number: a row of zeros stays dividable. NaN stays NaN.
+      const float scale = max_nan(amax[v] / 448.f, 1.17549435e-38f);
       if (p.group128 ? c % 128 == 0 : c == 0) sc[p.group128 ? c / 128 : 0] = scale;
       const Quotients by(scale);
       if constexpr (VEC == 8) {

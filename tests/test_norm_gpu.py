@@ -287,3 +287,22 @@ def test_backward_of_long_rows_off_8_columns(norm, D, dtype, out):
     r = norm.rmsnorm_backward(dy.cuda(), x.cuda(), w.cuda(), ds.cuda(), eps=1e-3)
     assert ref.rrms(r["dx"], want[0]) <= bound(dtype, D) * 4
     assert ref.rrms(r["dweight"], want[1]) <= bound(F32, D) * (1 + M ** 0.5)
+
+
+@pytest.mark.parametrize("D", [256, 300, 257, 4096, 1501])
+@pytest.mark.parametrize("group", [0, 128])
+def test_the_scale_of_nan_is_nan(norm, D, group):
+    """max |y| / 448 over values with a NaN among them is NaN, for a row as for 128 columns."""
+    x = torch.randn(4, D, device="cuda")
+    x[2, D - 1] = float("nan")                 # through the sum of squares, all of row 2
+    w = torch.ones(D, device="cuda")
+    y, scale, _ = norm.rmsnorm_fp8(x, w, group=group)
+    assert scale[2].isnan().all() and y[2].float().isnan().all()
+    keep = [0, 1, 3]
+    assert scale[keep].isfinite().all() and y[keep].float().isfinite().all()
+    w[130] = float("nan")                      # one column of every row
+    y, scale, _ = norm.rmsnorm_fp8(x[keep], w, group=group)
+    assert y[:, 130].float().isnan().all()
+    assert scale[:, 1 if group else 0].isnan().all()
+    if group:
+        assert scale[:, 0].isfinite().all() and y[:, :128].float().isfinite().all()
