@@ -36,8 +36,10 @@ int launch_fwd(NormParams p, cudaStream_t s) {
   p.W = (p.D + per_warp - 1) / per_warp;
   const int rows = p.W == 1 ? kRowsPerCta : 1;
   const unsigned blocks = (unsigned)(((long long)p.M + rows - 1) / rows);
-  if (32 * p.W * rows > ttt::norm_fwd_threads<VEC, VPT>()) return TTT_ERR_UNSUPPORTED;
-  ttt::norm_fwd_kernel<XT, RT, YT, VEC, VPT><<<blocks, 32 * p.W * rows, 0, s>>>(p);
+  if constexpr (VEC == 1)
+    ttt::norm_fwd_single_kernel<XT, RT, YT><<<blocks, 32 * p.W * rows, 0, s>>>(p);
+  else
+    ttt::norm_fwd_kernel<XT, RT, YT, VPT><<<blocks, 32 * p.W * rows, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 

@@ -65,9 +65,9 @@ __device__ __forceinline__ float warp_max(float x) {
 // x / scale, rounded once, for many x and one scale. The product with 1 / scale alone is an fp32 rounding
 // off and takes two codes in a million to the other side of the middle between two; corrected
 // by its exact remainder it is the quotient (P. Markstein, IBM J. Res. Dev. 34, 1990: y = 1 / scale correctly
-// rounded, q = x y, q - (q scale - x) y) for two more paired multiply-adds: 65536 rows of 2048 take 157 us, with the
-// product alone 152, with divisions 174. The remainder of small numbers is not exact, so scales
-// below 2^-80, and those that are no numbers, divide.
+// rounded, q = x y, q - (q scale - x) y) for two more paired multiply-adds: 65536 rows of 2048 take 150 us, with the
+// product alone 148, with divisions 164 (single columns divide). The remainder of small numbers is not
+// exact, so scales below 2^-80, and those that are no numbers, divide.
 struct Quotients {
   float scale, y;
   bool plain;
@@ -89,22 +89,8 @@ __device__ __forceinline__ int norm_column(int warp, int lane, int v) {
   return ((warp * VPT + v) * 32 + lane) * VEC;
 }
 
-// The most threads a forward launch takes: rows of up to 16384 single columns in 32 warps; of 8
-// columns a lane in 16 warps of 1024 columns or 8 of 512.
-template <int VEC, int VPT>
-constexpr int norm_fwd_threads() {
-  return VEC == 1 ? 1024 : VPT == 4 ? 512 : 256;
-}
-// Of those that an SM has to hold (0: as it comes). The 32 columns a lane of VPT = 4 otherwise take a few
-// registers more than 64: 65536 rows of 2048 in bf16 183 us, so 157; in 8 bits 158, so 150.
-template <int VEC, int VPT>
-constexpr int norm_fwd_ctas() {
-  return VEC == 1 ? 1 : VPT == 4 ? 2 : 0;
-}
-
 template <typename XT, typename RT, typename YT, int VEC, int VPT>
-__global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VEC, VPT>())
-    norm_fwd_kernel(const NormParams p) {
+__device__ __forceinline__ void norm_fwd(const NormParams& p) {
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31;
   const int warp = (threadIdx.x >> 5) % p.W, sub = (threadIdx.x >> 5) / p.W;
@@ -219,8 +205,8 @@ __global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VE
       // At least the smallest normal number: a row of zeros stays dividable. NaN stays NaN.
       const float scale = max_nan(amax[v] / 448.f, 1.17549435e-38f);
       if (p.group128 ? c % 128 == 0 : c == 0) sc[p.group128 ? c / 128 : 0] = scale;
-      const Quotients by(scale);
       if constexpr (VEC == 8) {
+        const Quotients by(scale);
         uint32_t q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -228,10 +214,24 @@ __global__ void __launch_bounds__(norm_fwd_threads<VEC, VPT>(), norm_fwd_ctas<VE
                                           __NV_E4M3);
         *reinterpret_cast<uint2*>(yp + c) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
       } else {
-        yp[c] = __nv_cvt_float_to_fp8(by(make_float2(s[v][0], 0.f)).x, __NV_SATFINITE, __NV_E4M3);
+        yp[c] = __nv_cvt_float_to_fp8(s[v][0] / scale, __NV_SATFINITE, __NV_E4M3);
       }
     }
   }
+}
+
+// The entries hold the registers to what the largest launch may have: a row of 16384 columns takes 16 warps of
+// four vectors a lane, or 32 warps of single columns.
+// Four vectors a lane otherwise take a few registers more than 64 (65536 rows of 2048: bf16 183 us, so 157;
+// in 8 bits 158, so 150). Single columns are at most 48: 32768 rows of 1535 in bf16 115 us and in 8 bits 158; with 64,
+// loads are brought forward at the price of warps, 122 and 165.
+template <typename XT, typename RT, typename YT, int VPT>
+__global__ void __launch_bounds__(VPT == 4 ? 512 : 256, VPT == 4 ? 2 : 0) norm_fwd_kernel(const NormParams p) {
+  norm_fwd<XT, RT, YT, 8, VPT>(p);
+}
+template <typename XT, typename RT, typename YT>
+__global__ void __maxnreg__(48) norm_fwd_single_kernel(const NormParams p) {
+  norm_fwd<XT, RT, YT, 1, 16>(p);
 }
 
 // Backward. A CTA of W warps walks rows blockIdx.x, blockIdx.x + gridDim.x, ..., one at
