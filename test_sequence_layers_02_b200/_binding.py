@@ -121,8 +121,10 @@ def strides_of(count: int, *parts):
     return arrays[count](*values)
 
 
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Torch's private calls, without the public ones' work around them; a release that lacks them has those.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+               (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 class On:

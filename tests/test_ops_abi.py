@@ -204,3 +204,22 @@ def test_partial_sums_beyond_what_their_reduction_counts(libs):
         parts = libs["conv"].ttt_conv_backward_workspace_bytes(B, 1, T, 1, 2) // 12
         assert 1 << 30 < parts < 1 << 31
         assert libs["conv"].ttt_conv_backward(*a.values(), None) == UNSUPPORTED
+
+
+def test_bindings_without_torch_s_private_calls(monkeypatch):
+    """Where a torch release has not the two private calls that shorten a call, its public ones are taken."""
+    import importlib.util
+    import types
+
+    import torch
+
+    from test_sequence_layers_02_b200 import _binding
+    spec = importlib.util.spec_from_file_location("test_sequence_layers_02_b200._binding_public", _binding.__file__)
+    module = importlib.util.module_from_spec(spec)
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec.loader.exec_module(module)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=700 + dev))
+    with module.On(3, None, ()) as stream:
+        assert stream == 703
