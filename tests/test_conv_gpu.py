@@ -330,3 +330,71 @@ def test_an_infinite_input_stays_in_its_own_products(conv, T, lengths, K):
     got, want = r["dweight"].clone(), want.clone()
     got[5, K - 1] = want[5, K - 1] = 0
     assert ref.rrms(got, want) <= bound(F32, K) * (1 + (B * T) ** 0.5)
+
+
+def plain(p, silu):
+    """The 64-bit form over whole tensors, on the GPU: windows of [state, x]. y, and the padded inputs."""
+    x, T, K = p["x"].double(), p["x"].shape[1], p["weight"].shape[1]
+    if p["lengths"] is not None:
+        x = torch.where((torch.arange(T, device="cuda") < p["lengths"][:, None])[..., None], x, torch.zeros_like(x))
+    ext = torch.cat((p["state"].double(), x), 1)
+    pre = p["bias"].double() + sum(p["weight"].double()[:, j] * ext[:, j:j + T] for j in range(K))
+    return (ref.silu(pre) if silu else pre), ext
+
+
+@pytest.mark.parametrize("D", [256, 65])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_tokens(conv, dtype, K, D):
+    """Enough tokens for runs of 32 a thread, four batches of loads each, with a ragged end."""
+    B, T = 3, 12643
+    assert D // (4 if D % 4 == 0 else 1) * B * T >= 148 * 16 * 32 * 32     # the rule of those runs
+    lengths = [T, 12000, 6677]
+    p = cuda(problem(B, T, D, K, dtype, seed=K, lengths=lengths))
+    y, st = conv.causal_conv(p["x"], p["weight"], p["bias"], silu=True, state=p["state"], lengths=p["lengths"])
+    want, ext = plain(p, True)
+    for b, n in enumerate(lengths):
+        # every stretch of tokens by itself: an error in one run is not averaged over the others
+        for a in range(0, n, 997):
+            e = min(n, a + 997)
+            assert ref.rrms(y[b, a:e], want[b, a:e]) <= bound(dtype, K), (b, a)
+        assert not y[b, n:].any()
+        assert torch.equal(st[b].double(), ext[b, n:n + K - 1])
+    # into heads
+    if D == 256:
+        heads = lambda t: t.unflatten(-1, (4, 64)).transpose(1, 2)  # noqa: E731
+        y2, st2 = conv.causal_conv(heads(p["x"]), p["weight"].view(4, 64, K), p["bias"].view(4, 64), silu=True,
+                                   state=heads(p["state"]), lengths=p["lengths"])
+        assert torch.equal(y2, heads(y)) and torch.equal(st2, heads(st))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D,K", [(2, 6007, 512, 4), (3, 4003, 387, 3), (8, 4099, 768, 2), (4, 4099, 767, 4)])
+def test_backward_in_longer_segments(conv, B, T, D, K, dtype):
+    """Sizes whose segments are longer than 8 tokens and not a whole number of load batches."""
+    blocks = conv.backward_workspace_bytes(B, 1, T, D, K) // (4 * B * D * (K + 1))
+    segments = [s for s in range(8, 65) if -(-T // (8 * s)) == blocks]
+    assert segments and min(segments) > 8
+    lengths = [T] + [max(1, T * (B - i) // (B + 1) - 1) for i in range(B - 1)]
+    p = cuda(problem(B, T, D, K, dtype, seed=T, lengths=lengths))
+    g = torch.Generator().manual_seed(1)
+    dy = torch.randn(B, T, D, generator=g).to(dtype).cuda()
+    dst = torch.randn(B, K - 1, D, generator=g).to(dtype).cuda()
+    leaves = {k: torch.nan_to_num(p[k].double(), nan=0.0).requires_grad_() for k in ("x", "weight", "bias", "state")}
+    y, ext = plain(dict(leaves, lengths=p["lengths"]), True)
+    there = (torch.arange(T, device="cuda") < p["lengths"][:, None])[..., None]
+    loss = (y * torch.where(there, dy.double(), torch.zeros_like(y))).sum()
+    loss = loss + sum((ext[b, n:n + K - 1] * dst[b].double()).sum() for b, n in enumerate(lengths))
+    want = dict(zip(("dx", "dweight", "dbias", "dstate"), torch.autograd.grad(loss, list(leaves.values()))))
+    for b, n in enumerate(lengths):
+        dy[b, n:] = float("nan")
+    r = conv.causal_conv_backward(p["x"], p["weight"], p["bias"], dy, dst, silu=True, state=p["state"],
+                                  lengths=p["lengths"])
+    for b, n in enumerate(lengths):
+        for a in range(0, n, 499):
+            e = min(n, a + 499)
+            assert ref.rrms(r["dx"][b, a:e], want["dx"][b, a:e]) <= bound(dtype, K) * 2, (b, a)
+        assert not r["dx"][b, n:].any()
+    assert ref.rrms(r["dstate"], want["dstate"]) <= bound(dtype, K) * 2
+    for k in ("dweight", "dbias"):
+        assert ref.rrms(r[k], want[k]) <= bound(F32, K) * (1 + (B * T) ** 0.5), k
