@@ -500,3 +500,128 @@ def test_one_token_of_a_token_major_batch(ssm):
     y2, h2, ck2 = ssm.selective_scan(*args(far), h0=c["h0"], want_chunks=True)
     r2 = ssm.selective_scan_backward(*args(far), ck2, dy, h)
     assert torch.equal(y, y2) and torch.equal(h, h2) and all(torch.equal(r[k], r2[k]) for k in r)
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, BF16), (F32, BF16)])
+def test_step_of_a_large_batch(ssm, N, dtype, out):
+    """Enough rows for several of them a thread (a batch that leaves a remainder): every row by itself."""
+    B, C, G = 303, 520, 2
+    p = problem(B, 1, C, N, dtype, G=G, seed=N)
+    one = cuda({k: v[:, 0] if k in ("u", "delta", "Bm", "Cm", "z") else v for k, v in p.items()})
+    on = (torch.rand(B, generator=torch.Generator().manual_seed(N)) < 0.7).to(torch.uint8)
+    on[-3:] = torch.tensor([1, 0, 1], dtype=torch.uint8)
+    ry, rh = ref.scan(*args(clean(p)), ref.up(p["h0"]), on.int())
+    h, y = one["h0"].clone(), torch.full((B, C), 5.0, dtype=out, device="cuda")
+    ssm.selective_step(*args(one), h, active=on.cuda(), y=y)
+    h2 = one["h0"].clone()
+    y2 = ssm.selective_step(*args(one), h2, active=on.cuda(), out_dtype=out)
+    assert torch.equal(h, h2)
+    for b in range(B):
+        if on[b]:
+            assert ref.rrms(y[b], ry[b, 0]) <= ref.tol(out, 1), b
+            assert ref.rrms(h[b], rh[b]) <= ref.tol(F32, 1), b
+            assert torch.equal(y[b], y2[b])
+        else:
+            assert (y[b] == 5).all() and not y2[b].any() and torch.equal(h[b], one["h0"][b]), b
+    # all rows, no options, and a single element off the packs
+    h3 = one["h0"].clone()
+    wide = torch.zeros(B, G * N + 1, dtype=dtype, device="cuda")
+    wide[:, 1:] = one["Bm"].flatten(1)
+    y3 = ssm.selective_step(one["u"], one["delta"], one["A"], wide[:, 1:].unflatten(1, (G, N)), one["Cm"], None, None, None,
+                            h3, out_dtype=out)
+    q = clean(p)
+    ry, rh = ref.scan(q["u"], q["delta"], q["A"], q["Bm"], q["Cm"], None, None, None, q["h0"], None)
+    for b in range(B):
+        assert ref.rrms(y3[b], ry[b, 0]) <= ref.tol(out, 1) and ref.rrms(h3[b], rh[b]) <= ref.tol(F32, 1), b
+
+
+@pytest.mark.parametrize("C,G,N", [(24, 3, 16), (21, 3, 16), (40, 2, 8), (16, 2, 32)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_split_prompts_with_groups_strides_and_lengths(ssm, C, G, N, dtype):
+    """Tokens over a cluster of CTAs, with slices of projections for inputs, groups and a ragged batch."""
+    B, T = 3, 411
+    p = problem(B, T, C, N, dtype, G=G, seed=C, lengths=[411, 130, 3])
+    c = cuda(p)
+    wide = torch.empty(B, T, 3 * C, dtype=dtype, device="cuda")
+    proj = torch.empty(B, T, 2 * G * N, dtype=dtype, device="cuda")
+    for i, k in enumerate(("u", "z", "delta")):
+        wide[..., i * C:(i + 1) * C] = c[k]
+        c[k] = wide[..., i * C:(i + 1) * C]
+    for i, k in enumerate(("Bm", "Cm")):
+        proj[..., i * G * N:(i + 1) * G * N] = c[k].flatten(2)
+        c[k] = proj[..., i * G * N:(i + 1) * G * N].unflatten(2, (G, N))
+    y, h, ck = ssm.selective_scan(*args(c), h0=c["h0"], lengths=c["lengths"], want_chunks=True)
+    q = clean(p)
+    leaves = [q[k].requires_grad_() for k in NAMES + ("h0",)]
+    ry, rh = ref.scan(*leaves, q["lengths"])
+    for b, n in enumerate(p["lengths"].tolist()):
+        assert ref.rrms(y[b, :n], ry[b, :n]) <= ref.tol(dtype, n) and not y[b, n:].any()
+        assert ref.rrms(h[b], rh[b]) <= ref.tol(F32, n)
+    g = torch.Generator().manual_seed(1)
+    dy, dh = torch.randn(B, T, C, generator=g).to(dtype), torch.randn(B, C, N, generator=g)
+    want = ref.gradients((ry, rh), (ref.up(dy), ref.up(dh)), leaves)
+    two = torch.full((B, T, 2 * C), float("nan"), dtype=dtype)
+    for b, n in enumerate(p["lengths"].tolist()):
+        two[b, :n, C:] = dy[b, :n]
+    r = ssm.selective_scan_backward(*args(c), ck, two.cuda()[..., C:], dh.cuda(), lengths=c["lengths"])
+    terms = {"dA": B * T, "dD": B * T, "ddelta_bias": B * T, "dBm": C // G, "dCm": C // G}
+    for k, w in zip(GRADS, want):
+        assert ref.rrms(r[k], w) <= ref.tol(r[k].dtype, T, terms.get(k, N)), k
+
+
+def straight(p, grads=None):
+    """The reference's form in fp32, and its error against 64 bits: outputs, and gradients for ``grads``."""
+    res = []
+    for up in (lambda t: t.detach().clone(), ref.up):
+        leaves = [None if p[k] is None else up(p[k]).requires_grad_(grads is not None) for k in NAMES + ("h0",)]
+        out = ref.scan(*leaves[:8], leaves[8], None)
+        if grads is not None:
+            out = tuple(out) + tuple(ref.gradients(out, [up(g) for g in grads], leaves))
+        res.append(out)
+    return res[1], [ref.rrms(a, b) for a, b in zip(*res)]
+
+
+# Eight times the error of a straight fp32 evaluation (a decay here is one ex2, four times as far off as exp
+# may be, of a rounded argument, and sums are taken in another order), and 2^-21 where that one
+# happens to be exact. Steps or states held in bf16 or tf32 are off by 2^-9 or 2^-12.
+def close_as_fp32(got, want, error, what):
+    assert ref.rrms(got, want) <= 8 * error + 2.0 ** -21, (what, ref.rrms(got, want), error)
+
+
+@pytest.mark.parametrize("B,T,C,N", [(2, 100, 40, 16), (2, 1500, 24, 8), (80, 300, 33, 16), (1, 9001, 8, 16), (2, 700, 12, 64)])
+def test_as_exact_as_fp32(ssm, B, T, C, N):
+    p = problem(B, T, C, N, F32, seed=T)
+    c = cuda(p)
+    y, h = ssm.selective_scan(*args(c), h0=c["h0"])
+    want, error = straight(p)
+    close_as_fp32(y, want[0], error[0], "y")
+    close_as_fp32(h, want[1], error[1], "h")
+
+
+@pytest.mark.parametrize("B,T,C,N", [(2, 90, 40, 16), (1, 500, 24, 8), (2, 333, 12, 32)])
+def test_gradients_as_exact_as_fp32(ssm, B, T, C, N):
+    p = problem(B, T, C, N, F32, seed=T)
+    g = torch.Generator().manual_seed(1)
+    dy, dh = torch.randn(B, T, C, generator=g), torch.randn(B, C, N, generator=g)
+    c = cuda(p)
+    _, _, ck = ssm.selective_scan(*args(c), h0=c["h0"], want_chunks=True)
+    r = ssm.selective_scan_backward(*args(c), ck, dy.cuda(), dh.cuda())
+    want, error = straight(p, (dy, dh))
+    for k, w, e in zip(GRADS, want[2:], error[2:]):
+        close_as_fp32(r[k], w, e, k)
+
+
+def test_decays_have_no_bias(ssm):
+    """A state without input, 112 tokens of one decay: the mean error of a decay between 0.7 and 1 stays within 0.2
+    units of 2^-24. 16384 decays in each of six ranges: their mean is known to 0.01 units (each
+    is off by up to 2 units and the products by half a unit a token, of either sign)."""
+    T, C, N = 112, 1024, 16
+    for lo, hi in ((0.70, 0.75), (0.75, 0.80), (0.80, 0.85), (0.85, 0.90), (0.90, 0.95), (0.95, 0.999)):
+        a = torch.rand(C, N, generator=torch.Generator().manual_seed(int(lo * 100)), dtype=torch.float64) * (hi - lo) + lo
+        A = torch.log(a).float()
+        one, zero = torch.ones(1, T, C, device="cuda"), torch.zeros(1, T, C, device="cuda")
+        v = torch.zeros(1, T, N, device="cuda")
+        _, h = ssm.selective_scan(zero, one, A.cuda(), v, v, softplus=False, h0=torch.ones(1, C, N, device="cuda"))
+        units = (torch.log(ref.up(h)[0]) - T * A.double()).mean() / T * 2 ** 24
+        assert abs(units) <= 0.2 + 0.01, (lo, float(units))
