@@ -111,13 +111,20 @@ __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x),
 // A log2 e, kept finite: with an infinite one a step of 0 would decay by exp(0 inf), which is no number. So an
 // A beyond 2.35e38 counts as that (its decay over any step above 1e-36 is 0 either way).
 __device__ __forceinline__ float scaled_rate(float A) {
+  constexpr float kMax = 3.402823466e38f;
+  const float x = A * kLog2e;
+  return x < -kMax ? -kMax : x > kMax ? kMax : x;
+}
+__device__ __forceinline__ float2 scaled_rate2(float2 A) {
+  return make_float2(scaled_rate(A.x), scaled_rate(A.y));
+}
+// The same in fewer instructions, for the step, which does it for every few rows (512 x 2048 channels: 22.4 us, with the
+// form above 23.5). The prompt's loop comes out slower with it: 1.37 against 1.32 ms for two of 32768 by 2048.
+__device__ __forceinline__ float scaled_rate_step(float A) {
   float x = A * kLog2e;  // (and NaN stays NaN)
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(3.402823466e38f));
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-3.402823466e38f));
   return x;
-}
-__device__ __forceinline__ float2 scaled_rate2(float2 A) {
-  return make_float2(scaled_rate(A.x), scaled_rate(A.y));
 }
 
 // exp(dt A), the decay of one token, for A scaled by log2 e.
@@ -683,8 +690,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
   const int g = cc / p.per_group;
   const size_t par = (size_t)cc * N + n0;
   State4 A = load_state(p.A + par);
-  A.lo = scaled_rate2(A.lo);
-  A.hi = scaled_rate2(A.hi);
+  A.lo = make_float2(scaled_rate_step(A.lo.x), scaled_rate_step(A.lo.y));
+  A.hi = make_float2(scaled_rate_step(A.hi.x), scaled_rate_step(A.hi.y));
   const float bias = p.delta_bias ? p.delta_bias[cc] : 0.f;
   const float skip = p.skip ? p.skip[cc] : 0.f;
   const int mine = Sum::first(lane % L);  // the row of this lane's scalars
