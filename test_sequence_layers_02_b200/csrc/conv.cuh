@@ -270,11 +270,13 @@ __global__ void __launch_bounds__(32 * kConvSegs, 2) conv_bwd_kernel(const ConvP
 #pragma unroll
           for (int q = 0; q < K; ++q) a.fma(w[q], win[(j - (K - 1) + q) & 3]);
           const V sg = a.sigmoid();
-          // SiLU'(a) = s (1 + a (1 - s)) = s + a s - (a s) s
-          a.mul(sg);
-          V d = sg;
-          d.add(a);
-          d.fma_minus(a, sg);
+          // SiLU'(a) = s (1 + a (1 - s)): 1 - s is exact where a is large, and s + a s - a s s is not
+          V rest, d;
+          rest.set(1.f);
+          d.set(1.f);
+          rest.fma_minus(sg, d);
+          d.fma(a, rest);
+          d.mul(sg);
           g.mul(d);
         }
         if (!inner && t >= len) g = zero;

@@ -398,3 +398,32 @@ def test_backward_in_longer_segments(conv, B, T, D, K, dtype):
     assert ref.rrms(r["dstate"], want["dstate"]) <= bound(dtype, K) * 2
     for k in ("dweight", "dbias"):
         assert ref.rrms(r[k], want[k]) <= bound(F32, K) * (1 + (B * T) ** 0.5), k
+
+
+@pytest.mark.parametrize("D", [8, 5])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_slope_of_silu_over_its_whole_range(conv, dtype, D):
+    """Values before the activation from 1e-3 to 1e30, of either sign, element by element: the slope is
+    s (1 + x (1 - s)), 1 for a large x. With s from an ex2 whose argument is rounded, s is off by up to
+    2^-21 + |x| 2^-23 of itself for x < 0; its two terms and their sum round three times more."""
+    T = 400
+    mag = torch.logspace(-3, 30, T // 2)
+    x = torch.cat((mag, -mag))[None, :, None].expand(1, T, D).to(dtype).contiguous()
+    x[:, ::7] = x[:, ::7].clamp(-12, 12)
+    weight = torch.zeros(D, 2)
+    weight[:, 1] = 1                                     # pre = x
+    g = torch.Generator().manual_seed(6)
+    dy = torch.randn(1, T, D, generator=g)
+    r = conv.causal_conv_backward(x.cuda(), weight.cuda(), None, dy.cuda(), silu=True)
+    v, gy = ref.up(x), ref.up(dy)
+    s = torch.sigmoid(v)
+    want = gy * s * (1 + v * (1 - s))
+    room = 2.0 ** -21 + v.clamp(min=-200, max=0).abs() * 2.0 ** -23 + 3 * 2.0 ** -24
+    # For x > 0, s = 1 / (1 + e) is off by the rounding of 1 + e (2^-24) and the reciprocal (2^-23), and x (1 - s) by
+    # x times that; from x = 17 on e < 2^-24, so that s is 1 and the term, at most 17 e^-17, is 0.
+    room = room + v.clamp(min=0, max=17) * (2.0 ** -23 + 2.0 ** -24)
+    if dtype == BF16:
+        room = room + ref.BF16
+    size = gy.abs() * s * (1 + v.abs() * (1 - s))        # of the terms: they cancel at x = -1.28
+    # (below the smallest normal numbers s is 0)
+    assert ((ref.up(r["dx"]) - want).abs() <= room * size + 1e-35).all()
