@@ -9,7 +9,7 @@
  * s goes out in the residual stream's type, y (from the unrounded s) as fp32,
  * bf16, or 8 bits (e4m3) with fp32 scales: for each row, or for each 128 columns
  * of it, scale = max |y| / 448 (at least the smallest normal fp32, so that it can be
- * divided by) and code = e4m3(y / scale), the fp32 quotient to nearest. The 8-bit form is
+ * divided by; NaN with a NaN among them) and code = e4m3(y / scale), the fp32 quotient to nearest. The 8-bit form is
  * what the projections behind the norm take in serving.
  *
  * Status codes are those of ttt_scan.h. Every call only enqueues work on

@@ -4,6 +4,10 @@ Each of these operators runs on CUDA tensors only, on ``stream`` (default: the c
 tensors' device), and returns without synchronising. Outputs and workspaces that a call makes itself
 are allocated on that stream; inputs are marked as used by it where it is not the current one.
 
+The calls are outside autograd, as ``ttt_scan``'s are: their outputs carry no ``grad_fn``, also for inputs that
+require a gradient, and gradients come from the ``*_backward`` calls, made by hand (or from a
+``torch.autograd.Function`` of the caller's around both).
+
 A one-token step takes the GPU a few microseconds, so these checks are written for few and cheap
 calls into torch: a tensor's device by its number, contiguity before strides.
 """

@@ -8,7 +8,8 @@ Tensors are [B, T, D], or [B, H, T, d] with weight [H, d, K] and bias [H, d], th
 scan. A row of channels is contiguous; batch rows, heads and tokens may have any strides, so a
 token-major projection can be given as ``x.unflatten(-1, (H, d)).transpose(1, 2)`` and comes out as
 the contiguous [B, H, T, d] that ``ttt_scan.scan`` takes. CUDA tensors only; see ``_binding`` for
-streams. There is no CPU fallback.
+streams. There is no CPU fallback. Nothing is recorded for autograd: gradients come from
+``causal_conv_backward``, called by hand.
 """
 
 from __future__ import annotations

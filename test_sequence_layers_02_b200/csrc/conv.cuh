@@ -7,10 +7,12 @@
 // registers, so an input is read from memory once (and K - 1 tokens again at the
 // start of a run, from cache), while the next batch of loads is under way.
 //
-// Measured, bf16, K = 4: 2 x 32768 tokens by 2048 channels into heads 105 us (537 MB: 78 % of the copy
-// bandwidth; with batches of 4 tokens 110 us); forward and backward of 8 x 4096 tokens by 768 channels, ragged,
-// 71 us, of which the backward's kernel 47 us: its windows, weights and weight sums take 128
-// registers, so 16 warps an SM, and latency is what is left; one token for 512 rows of 2048 channels 5.5 us.
+// Measured, K = 4: 2 x 32768 tokens by 2048 channels into heads in bf16 105 us (537 MB: 78 % of the copy
+// bandwidth; with batches of 4 tokens 110 us), in fp32 203 us (1074 MB: 81 %; two batches of 8 packs of fp32 do not fit
+// 96 registers, up to 192 bytes a thread are spilled); forward and backward of 8 x 4096 tokens by 768 channels, ragged,
+// bf16, 71 us, of which the backward's kernel 48 us: its windows, weights and weight sums take 128
+// registers (and spill 16 bytes, in fp32 208), so 16 warps an SM, and latency is what is left (in fp32 the
+// backward takes 99 us for 302 MB); one token for 512 rows of 2048 channels 5.5 us, 6.3 us with inputs and states out of HBM.
 #pragma once
 
 #include "seq_common.cuh"

@@ -5,11 +5,15 @@
 // lane holds VPT groups of 8 neighbouring columns and a row takes W warps; rows of
 // up to 1024 columns fit one warp, which then needs no barrier at all, and four
 // such rows share a CTA. Rows whose pointers or strides are off 16 bytes, or
-// with D not a multiple of 8, take the same kernel with single columns.
+// with D not a multiple of 8, take the same kernel with single columns, at about half the speed in bf16.
 //
 // Measured, bf16: 65536 rows of 2048 in 8 bits, a scale for each 128 columns, 150 us (944 MB: 96 % of the copy
-// bandwidth); 32768 rows of 1536 forward 58 us (403 MB: 105 %, part of it still in L2) and backward
-// 72 us and 8 us for the sum of the weight gradients' parts; 64 rows of 2048 in 8 bits 3.8 us.
+// bandwidth; 164 in a long run of calls); 32768 rows of 1536 forward 61 us (403 MB: 101 %, part of it still in L2) and
+// backward 72 us and 8 us for the sum of the weight gradients' parts; the same with 1535 columns 115 us, in 8 bits 158
+// (69 at 1536), backward 133. fp32, 32768 rows of 1536: 121 and 124 us. 64 rows of 2048 in 8 bits 3.9 us. The backward
+// spills where a row takes more registers than its CTA leaves: 104 bytes a thread in fp32 beyond 2048 columns, 112 in
+// single columns, 376 to 840 beyond 8192, where 1024 threads have 64 registers (4096 rows of 16384, bf16: 371 us,
+// 82 for its bytes).
 #pragma once
 
 #include <cuda_fp8.h>

@@ -3,11 +3,12 @@
 //
 // Work: one exponential, one multiply and two multiply-adds for each of the N
 // states of every (token, channel), against four 2- or 4-byte elements of
-// traffic. At N = 16 the special-function units (16 lanes per clock and SM) bind first:
-// (N + 4) / 16 clocks per (token, channel) with the softplus and the gate counted,
+// traffic. With every exponential on the special-function units (16 lanes per clock and SM), as here, these bind
+// first at N = 16: (N + 4) / 16 clocks per (token, channel) with the softplus and the gate counted,
 // where HBM would take a quarter of that in bf16. Measured, bf16, N = 16: two prompts of 32768
-// tokens by 2048 channels 1.33 ms (0.59 ms at that bound, with 128 CTAs on 148 SMs); 16 of 2048 by
-// 1536 0.41 ms (0.22). What is left is the latency of the loop, about 80 clocks a token for
+// tokens by 2048 channels 1.32 ms (0.58 ms of special functions; 128 CTAs on 148 SMs), in fp32 1.39; 16 of 2048 by
+// 1536 0.41 ms (0.22). The SPLIT builds, and single elements at N = 8 and 32, spill up to 420 bytes a thread at
+// the 80 registers that two CTAs an SM leave. What is left is the latency of the loop, about 80 clocks a token for
 // a warp of the recurrence that shares its scheduler with staging and output, 57 alone; without
 // its exponentials it still takes 69.
 #pragma once
@@ -118,8 +119,8 @@ __device__ __forceinline__ float scaled_rate(float A) {
 __device__ __forceinline__ float2 scaled_rate2(float2 A) {
   return make_float2(scaled_rate(A.x), scaled_rate(A.y));
 }
-// The same in fewer instructions, for the step, which does it for every few rows (512 x 2048 channels: 22.4 us, with the
-// form above 23.5). The prompt's loop comes out slower with it: 1.37 against 1.32 ms for two of 32768 by 2048.
+// The same in fewer instructions, for the step, which does it for every few rows (512 x 2048 channels: 22.4 us,
+// with the form above 23.5). The prompt's loop comes out slower with it: 1.37 against 1.32 ms for two of 32768 by 2048.
 __device__ __forceinline__ float scaled_rate_step(float A) {
   float x = A * kLog2e;  // (and NaN stays NaN)
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(3.402823466e38f));
@@ -675,8 +676,10 @@ __global__ void __launch_bounds__(SsmFwdShape<N, P, InT, VEC>::NT, N < 64 ? 2 : 
 // everything else. So a thread takes the same states of ROWS batch rows, with one read of the
 // parameters and all loads on their way together, while a row's step size, gate and output
 // are worked out by one of the channel's lanes alone: the step size goes to the others by a
-// shuffle, the sums of the read-out scatter to the row's lane. (512 rows of 2048 channels, N = 16: 143 MB
-// in 22 us; with the scalars of every row in every lane 31 us.)
+// shuffle, the sums of the read-out scatter to the row's lane. (512 rows of 2048 channels, N = 16, bf16: 143 MB, 22 us
+// where the 67 MB of state are still in L2, as when one call follows another on it, with the scalars of every row
+// in every lane 31 us; 29 us in a run over the states of 8 layers, three quarters of the copy bandwidth, where the
+// loads' latency binds.)
 template <int L, typename InT, int VEC, int ROWS>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p) {
   constexpr int N = 4 * L;

@@ -25,8 +25,9 @@
 // The sums over channel tiles go through partial sums in global memory, added in tile
 // order. No atomics: the same bits on every call.
 //
-// Measured, bf16, N = 16, with the reductions: 8 x 4096 tokens by 768 channels 0.90 ms, 16 x 2048 by 1536
-// 1.35 ms, 4 x 2048 by 256 0.09 ms; about 0.47 instructions a clock and scheduler.
+// Measured, bf16, N = 16, with the reductions: 8 x 4096 tokens by 768 channels 0.90 ms (fp32 0.91), 16 x 2048 by 1536
+// 1.34 ms, 4 x 2048 by 256 0.09 ms; about half an instruction a clock and scheduler. At 128 registers the SPLIT
+// builds spill up to 80 bytes a thread and single elements at N = 8 up to 368; N = 64, at 168, up to 628.
 #pragma once
 
 #include "ssm.cuh"

@@ -4,8 +4,9 @@
 
 with y in fp32 or bf16 (``rmsnorm``, and ``rmsnorm_backward`` for training) or in 8 bits with scales for the
 projections behind it (``rmsnorm_fp8``). Rows are the last dimension; they are contiguous, and a
-2-D tensor may have any row stride. CUDA tensors only; see ``_binding`` for streams. There is no CPU
-fallback.
+2-D tensor may have any row stride from D up (rows of an expanded tensor have to be copied first). CUDA
+tensors only; see ``_binding`` for streams. There is no CPU fallback. Nothing is recorded for
+autograd: gradients come from ``rmsnorm_backward``, called by hand.
 """
 
 from __future__ import annotations
@@ -114,7 +115,8 @@ def rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
     """``(y, scale, s) = rmsnorm_fp8(x, weight, residual)``: y as float8_e4m3fn codes.
 
     scale: fp32 [..., 1], the row's max |y| / 448 (``group=0``), or [..., ceil(D / 128)], that of each 128
-    columns (``group=128``); the value of a code is code * scale. Otherwise as ``rmsnorm``.
+    columns (``group=128``); the value of a code is code * scale, and a code is that of the fp32 quotient y / scale. A
+    row or group with a NaN has NaN for its scale and codes. Otherwise as ``rmsnorm``.
     """
     if group not in (0, 128):
         raise ValueError("group: expected 0 (a scale per row) or 128")

@@ -8,7 +8,8 @@ for prompts (``selective_scan``), training (``selective_scan_backward``) and sin
 (``selective_step``). u, delta, z, y are [B, T, D], Bm and Cm [B, T, G, N] (or [B, T, N] for one
 group), fp32 or bf16, with contiguous rows and any strides between batch rows, tokens and groups;
 parameters and states are fp32. CUDA tensors only; see ``_binding`` for streams. There is no CPU
-fallback.
+fallback. Nothing is recorded for autograd: gradients come from ``selective_scan_backward``, called
+by hand.
 """
 
 from __future__ import annotations
