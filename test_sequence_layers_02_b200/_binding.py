@@ -50,6 +50,12 @@ def cuda_index(name: str, x: torch.Tensor) -> int:
     return x.get_device()
 
 
+def fit_ints(name: str, *sizes) -> None:
+    """The sizes of a call are C ints, to which ctypes would cut larger ones without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"{name}: sizes up to 2147483647, got {tuple(sizes)}")
+
+
 def _refuse(name, t, shape, dtype, dev, what):
     raise ValueError(f"{name}: expected {what} {tuple(shape)} {dtype} on cuda:{dev}, got "
                      f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")

@@ -19,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, fit_ints, like,
                        out_dtype_of, raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
@@ -48,6 +48,7 @@ def _sizes(x, weight, bias, dev, tokens: bool):
     else:
         raise ValueError("x must be [B, T, D] or [B, H, T, d]" if tokens else
                          "x must be [B, D] or [B, H, d]")
+    fit_ints("x", *shape)
     K = weight.shape[-1] if weight.dim() == len(channels) + 1 else 0
     w = check_whole("weight", weight, channels + (K,), _F32, dev)
     b = check_whole("bias", bias, channels, _F32, dev)

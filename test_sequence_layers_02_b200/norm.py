@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, fit_ints, like,
                        out_dtype_of, raise_for, workspace_of, arrays)
 from .ttt_scan import IN_BF16, OUT_BF16
 
@@ -58,7 +58,9 @@ def _shape(name, t):
     if not shape:
         raise ValueError(f"{name} must be [..., D]")
     D = shape[-1]
-    return shape, t.numel() // D if D else 0, D
+    M = t.numel() // D if D else 0
+    fit_ints(name, M, D)
+    return shape, M, D
 
 
 def _forward(x, weight, residual, eps, mode, group, y, y_dtype, s, stream):

@@ -19,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import (Library, On, check, check_float, check_whole, cuda_index, like,
+from ._binding import (Library, On, check, check_float, check_whole, cuda_index, fit_ints, like,
                        out_dtype_of, raise_for, strides_of, workspace_of)
 from .ttt_scan import IN_BF16, OUT_BF16
 
@@ -55,6 +55,7 @@ def _check(u, delta, A, Bm, Cm, D, z, delta_bias, dims):
     if Bm.dim() != dims + 1:
         raise ValueError("Bm must be [B, T, G, N] or [B, T, N] (a step: without T)")
     G = Bm.shape[-2]
+    fit_ints("u, Bm", G, N, *shape)
     bc = shape[:-1] + (G, N)
     return dev, G, N, Bm, Cm, (
         check("u", u, shape, dtype, dev), check("delta", delta, shape, dtype, dev),

@@ -223,3 +223,31 @@ def test_bindings_without_torch_s_private_calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=700 + dev))
     with module.On(3, None, ()) as stream:
         assert stream == 703
+
+
+def test_sizes_beyond_an_int_are_refused_by_the_bindings(monkeypatch):
+    """ctypes would cut 2^32 + 5 to 5: a call on 5 tokens that reports success. (Expanded tensors: no memory.)"""
+    import torch
+
+    from test_sequence_layers_02_b200 import conv, norm, ssm
+    for m in (conv, norm, ssm):
+        monkeypatch.setattr(m, "cuda_index", lambda name, x: -1)
+    for module in (conv._lib, norm._lib, ssm._lib):
+        for name in module._functions:
+            monkeypatch.setattr(module, name, lambda *a: pytest.fail("reached the library"), raising=False)
+    big = (1 << 32) + 5
+    row, w = torch.zeros(8), torch.zeros(8, 4)
+    A, bc = torch.zeros(8, 8), torch.zeros(8)
+    calls = [lambda: norm.rmsnorm(row.expand(big, 8), row), lambda: norm.rmsnorm_fp8(row.expand(1 << 16, 1 << 16, 8), row),
+             lambda: norm.rmsnorm_backward(row.expand(big, 8), row.expand(big, 8), row)]
+    for shape in ((1, big, 8), (big, 1, 8)):
+        x, v = row.expand(shape), bc.expand(shape)
+        calls += [lambda x=x: conv.causal_conv(x, w), lambda x=x: conv.causal_conv_backward(x, w, None, x),
+                  lambda x=x, v=v: ssm.selective_scan(x, x, A, v, v),
+                  lambda x=x, v=v: ssm.selective_scan_backward(x, x, A, v, v, None, None, None, None, x)]
+    x, v = row.expand(big, 8), bc.expand(big, 8)
+    calls += [lambda: conv.causal_conv_step(x, w, None, row.expand(big, 3, 8)),
+              lambda: ssm.selective_step(x, x, A, v, v, None, None, None, row.expand(big, 8, 8))]
+    for f in calls:
+        with pytest.raises(ValueError, match="2147483647"):
+            f()
